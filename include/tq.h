@@ -425,7 +425,7 @@ tq_status tq_attn_prefill(const tq_prefill_args* a, void* workspace, size_t ws_b
  * PolarQuant keys: TQ_ERR_UNSUPPORTED. A step appends token append_pos[b]
  * through the page table before it attends (an entry that holds nothing, or a
  * position past the table, skips that sequence's append); the page it writes
- * must be held by that sequence alone. */
+ * must be held by that sequence alone (tq_pages_reserve leaves it so). */
 typedef struct {
     int window;                /* 0: every token; else > 0                      */
     int sinks;                 /* >= 0                                          */
@@ -495,7 +495,11 @@ size_t tq_pages_workspace(const tq_page_pool* pool, int rows);
 
 /* Pages for the tokens lengths[b] .. lengths[b] + add[b] - 1 of every row:
  * entries of theirs that hold nothing take a free page each. Pages past
- * max_pages count as shortage. */
+ * max_pages count as shortage. So that the row can write these tokens: where
+ * they start in the middle of a page that other entries hold too (a row cut
+ * back to less than what it was forked with), the row takes a free page in its
+ * place as well, with a copy of the contents (with none free its entry is -1:
+ * the tokens in that page are lost to the row). */
 typedef struct {
     tq_page_pool pool;
     tq_page_table table;
@@ -527,7 +531,8 @@ tq_status tq_pages_trim(const tq_pages_trim_args* a, tq_stream stream);
  * pages of a row without children become free (for the next call). The rows
  * of dst must hold nothing (their former entries are overwritten, not given
  * back); dst and src do not overlap; dst.max_pages >= src.max_pages.
- * Every page that two rows share must be full in both. A child whose copy
+ * A row that is cut back into a page it shares gets its own copy from the next
+ * tq_pages_reserve, which comes before its next token. A child whose copy
  * finds no free page keeps its length, and its last tokens are not visible. */
 typedef struct {
     tq_page_pool pool;

@@ -729,7 +729,8 @@ def tq_pages_workspace(pool, rows):
 @_bindable("tq_pages_reserve")
 def tq_pages_reserve(pool, table, lengths, add, workspace, shortage=None):
     """Pages for the `add` tokens (an int, or device int32 per row) behind each
-    row's lengths[b] tokens."""
+    row's lengths[b] tokens; a half-filled last page that other rows hold too is
+    replaced by a copy."""
     a = tq_pages_reserve_args(pool.struct(), _table_struct(table), _int32_ptr(lengths, "lengths", table.shape[0]))
     if isinstance(add, int):
         a.add_all = add
@@ -1109,8 +1110,9 @@ class PagedKVCache:
         at_most (an int): and those behind the first at_most, which tells the
         host how long the rows are where it knows a lower bound than the tokens
         appended so far (the calls plan with it and refuse what would pass
-        max_tokens). A row whose window has moved on cannot get its old tokens
-        back."""
+        max_tokens). Rows may go back to less than they were forked with: the
+        page they go on in is copied by the next call that appends. A row whose
+        window has moved on cannot get its old tokens back."""
         import torch
 
         _int32_ptr(lengths, "lengths", self.batch)

@@ -293,6 +293,10 @@ __device__ __forceinline__ int64_t row_tokens(int n, const TableParams& t, int p
 
 // ---------------------------------------------------------------- reserve ---
 
+// Besides empty entries, a row asks for a page where its tokens go on in the
+// middle of one that another entry holds too: written there, they would
+// overwrite the other row's.
+
 // the pages [j0, j1) that the tokens length .. length + add - 1 of a row lie
 // in, and how many of them lie past the table
 __device__ __forceinline__ void reserve_range(const ReserveParams& p, int row, int* j0, int* j1, int* past) {
@@ -317,30 +321,44 @@ __global__ void __launch_bounds__(kPageThreads) reserve_count_kernel(const __gri
     if (row >= p.t.rows) return;
     int j0, j1, past, n = 0;
     reserve_range(p, row, &j0, &j1, &past);
-    for (int j = j0 + lane; j < j1; j += 32) n += page_ok(p.t.e[row * p.t.stride + j], p.pool.n_pages) ? 0 : 1;
+    const bool part = max(p.lengths[row], 0) % p.pool.page != 0;
+    bool own = false;  // lane 0: the half-filled last page is another entry's too, the row wants one of its own
+    for (int j = j0 + lane; j < j1; j += 32) {
+        const int e = p.t.e[row * p.t.stride + j];
+        bool ask = !page_ok(e, p.pool.n_pages);
+        if (j == j0 && part && !ask) ask = own = p.pool.refs[e] > 1;
+        n += ask ? 1 : 0;
+    }
     n = __reduce_add_sync(TQ_FULL_MASK, n);
-    if (lane == 0) p.need[row] = n;
+    if (lane == 0) p.need[row] = 2 * n + (own ? 1 : 0);
 }
 
-// one CTA per row
+// One CTA per row. A half-filled last page that another entry holds too is
+// copied to the page the row takes for it (all of the row's holders decide by
+// the counts as they stood, so where all of them take one the old page is free
+// after the call).
 __global__ void __launch_bounds__(kPageThreads) reserve_take_kernel(const __grid_constant__ ReserveParams p) {
     extern __shared__ int s_pre[];
+    __shared__ int s_from, s_to;
     wait_prior_grid();
     const int row = blockIdx.x;
     int j0, j1, past;
     reserve_range(p, row, &j0, &j1, &past);
-    const int want = p.need[row];
+    const int want = p.need[row] >> 1;
+    const bool own = p.need[row] & 1;
     if (threadIdx.x == 0 && past > 0 && p.shortage) atomicAdd(p.shortage, past);
     if (want == 0) return;
     load_prefix(p.ix, s_pre);
     int before = 0;
-    for (int r = threadIdx.x; r < row; r += kPageThreads) before += p.need[r];
+    for (int r = threadIdx.x; r < row; r += kPageThreads) before += p.need[r] >> 1;
     int rank = block_sum(before);  // this row's first request
     const int free_pages = s_pre[p.ix.segs];
     for (int j = j0; j < j1; j += kPageThreads) {
         const int jj = j + (int)threadIdx.x;
         int32_t* e = p.t.e + row * p.t.stride + jj;
-        const bool ask = jj < j1 && !page_ok(*e, p.pool.n_pages);
+        const int old = jj < j1 ? *e : -1;
+        const bool copy = own && jj == j0;
+        const bool ask = jj < j1 && (copy || !page_ok(old, p.pool.n_pages));
         int total;
         const int r = rank + block_prefix(ask ? 1 : 0, &total);
         if (ask) {
@@ -352,9 +370,19 @@ __global__ void __launch_bounds__(kPageThreads) reserve_take_kernel(const __grid
                 atomicAdd(p.shortage, 1);
             }
             *e = got;
+            if (copy) {
+                s_from = old;
+                s_to = got;
+            }
         }
         rank += total;
     }
+    if (!own) return;
+    __syncthreads();
+    const int from = s_from, to = s_to;
+    if (to >= 0)
+        for (int c = 0; c * kCopyUnits < p.pool.off[kPagePlanes]; ++c) copy_chunk(p.pool, p.pool, from, to, c);
+    if (threadIdx.x == 0) atomicSub(p.pool.refs + from, 1);
 }
 
 // ------------------------------------------------------------------- fork ---

@@ -47,7 +47,7 @@ struct ReserveParams {
     const int32_t* lengths;
     const int32_t* add;  // NULL: add_all for every row
     int add_all;
-    int32_t* need;       // [rows] requests of a row
+    int32_t* need;       // [rows] twice a row's requests, + 1 where the first is for a copy of its last page
     int32_t* shortage;   // may be NULL
 };
 

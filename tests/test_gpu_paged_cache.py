@@ -1,0 +1,167 @@
+"""The paged cache through what a serving loop does between its steps: rows cut
+back to less than they were forked with. Every output is compared with the same
+attention over contiguous caches that hold each row's own tokens; pages, counts
+and tables have to be equal to a sequential model's."""
+
+import numpy as np
+import pytest
+import torch
+
+from online_kv_cache_quantize_gb300 import binding as B
+from test_gpu_pages import Model, _contents, _gpu, _pool, _same, _ws
+
+pytestmark = pytest.mark.gpu
+
+# Both sides read the same codes and add the same fp32 terms, at most a few hundred of unit scale, in another
+# order: each is rounded to 2^-24 or split in fp16 halves to 2^-22, which stays far below this.
+TOL = 1e-4
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from online_kv_cache_quantize_gb300 import build
+    build.build()
+
+
+def _rand(r, *shape):
+    return torch.from_numpy(r.standard_normal(shape).astype(np.float32)).cuda().to(torch.bfloat16)
+
+
+class Histories:
+    """Contiguous caches with a row per sequence, whose tokens come and go on their own."""
+
+    def __init__(self, paged, cap):
+        self.p, self.cap, self.n = paged, cap, [0] * paged.batch
+        self.k = B.Cache("prod", 3, 128, rows=paged.batch * paged.hkv, capacity=cap)
+        self.v = B.Cache("mse", 3, 128, rows=paged.batch * paged.hkv, capacity=cap)
+
+    def append(self, k, v, count=None):
+        """k, v [batch, hkv, C, 128]; the first count[b] tokens (all) go to row b."""
+        c = k.shape[2]
+        count = [c] * len(self.n) if count is None else count
+        slots = np.full((len(self.n), self.p.hkv, c), -1, dtype=np.int64)
+        for b, n in enumerate(self.n):
+            for h in range(self.p.hkv):
+                slots[b, h, :count[b]] = (b * self.p.hkv + h) * self.cap + n + np.arange(count[b])
+            self.n[b] += count[b]
+        s = torch.from_numpy(slots.reshape(-1)).cuda()
+        B.tq_quantize_kv(self.k, self.p.rot, k.reshape(-1, 128), qjl=self.p.qjl, dst_slot=s)
+        B.tq_quantize_kv(self.v, self.p.rot, v.reshape(-1, 128), dst_slot=s)
+
+    def fork(self, parent):
+        for p in (self.k.codes, self.k.signs, self.k.norm, self.k.rnorm, self.v.codes, self.v.norm):
+            x = p.view(len(self.n), -1)
+            x.copy_(x[torch.tensor([max(i, 0) for i in parent], device="cuda")].clone())
+        self.n = [self.n[i] if i >= 0 else 0 for i in parent]
+
+    def attend(self, q):
+        out = torch.empty(q.shape, device="cuda")
+        a = (q, self.k, self.v, torch.tensor(self.n, dtype=torch.int32, device="cuda"), max(max(self.n), 1), self.p.rot,
+             self.p.qjl, out)
+        view = B.View(self.p.window, self.p.sinks)
+        B.tq_attn_decode_view(*a, B.workspace(B.tq_attn_decode_view_workspace(*a, view)), view)
+        return out
+
+    def step(self, r, hq):
+        """One step of both: the paged cache's output must be this one's."""
+        q, k, v = _rand(r, len(self.n), hq, 128), _rand(r, len(self.n), self.p.hkv, 128), _rand(r, len(self.n), self.p.hkv, 128)
+        out = self.p.step(q, k, v)
+        self.append(k[:, :, None], v[:, :, None])
+        err = float((out - self.attend(q)).abs().max())
+        assert err <= TOL, err
+        assert self.p.lengths.tolist() == self.n
+
+
+def _counts_match(p):
+    t = p.table[p.table >= 0].cpu().numpy()
+    assert np.array_equal(np.bincount(t, minlength=p.pool.n_pages), p.pool.refs.cpu().numpy())
+
+
+# ------------------------------------------- rows that go back below a fork ---
+@pytest.mark.parametrize("short", [0, 3, 4])
+@pytest.mark.parametrize("page,hkv", [(16, 2), (208, 8)])
+def test_reserve_copies_a_shared_last_page(page, hkv, short):
+    """Rows whose tokens go on in the middle of a shared page take a copy, in row order with the other requests;
+    a full shared page, a page of one holder and rows that add nothing keep theirs. Without a free page the
+    entry is empty, and counted."""
+    pool = _pool(9 - short, hkv=hkv, page=page, seed=5)
+    t = np.array([[3, 4, -1], [3, 4, 1], [3, 4, -1], [0, 4, -1], [3, 2, -1], [3, 4, -1]], dtype=np.int32)
+    lengths = np.array([page + 5, page + 9, 2 * page, page - 1, page + 3, 2 * page - 1])
+    add = np.array([2, 1, 1, 1, page, 0])
+    m = Model(9 - short, page)
+    for e in t[t >= 0]:
+        m.refs[e] += 1
+    pool.refs.copy_(_gpu(m.refs))
+    data, refs0, free, lost = _contents(pool), m.refs.copy(), m.free(), 0
+    want = t.copy()
+    for b in range(len(t)):
+        if not add[b]:
+            continue
+        for j in range(lengths[b] // page, -(-(lengths[b] + add[b]) // page)):
+            e = t[b, j]
+            own = j == lengths[b] // page and lengths[b] % page and e >= 0 and refs0[e] > 1
+            if e >= 0 and not own:
+                continue
+            got = m.take(free)
+            want[b, j] = got
+            lost += got < 0
+            if got >= 0:
+                m.refs[got] = 1
+            if own:
+                m.refs[e] -= 1
+                if got >= 0:
+                    data[got] = data[e]
+    assert lost == short
+    table, word = _gpu(t), torch.full((1,), 9, dtype=torch.int32, device="cuda")
+    B.tq_pages_reserve(pool, table, _gpu(lengths), _gpu(add), _ws(pool, len(t)), shortage=word)
+    _same(pool, m, ("table", table, want), ("shortage", word, [lost]))
+    assert np.array_equal(_contents(pool), data)
+
+
+@pytest.mark.parametrize("back", [[77, 77, 77], [77, 88, 64], [88, 3, 85], [0, 88, 16]])
+@pytest.mark.parametrize("again", [False, True])
+def test_rows_go_back_below_a_fork(back, again):
+    """A prompt of 80 tokens forked to every row, some tokens each, then rows cut back into pages that they
+    share (all of them, some, to a page's start, to nothing), and different tokens from there on; also
+    forked again before they go on."""
+    r = np.random.default_rng(sum(back))
+    hq, hkv = 4, 2
+    p = B.PagedKVCache(3, hq, hkv, n_pages=40, max_tokens=160, page=16)
+    ref = Histories(p, 160)
+    q, k, v = _rand(r, 3, 80, hq, 128), _rand(r, 3, hkv, 80, 128), _rand(r, 3, hkv, 80, 128)
+    p.prefill_chunk(q, k, v)
+    ref.append(k, v)
+    p.fork(_gpu([1, 1, 1]))
+    ref.fork([1, 1, 1])
+    for _ in range(8):
+        ref.step(r, hq)
+    p.rollback(_gpu(back))
+    ref.n = list(back)
+    if again:
+        p.fork(_gpu([0, 0, 1]))
+        ref.fork([0, 0, 1])
+    for _ in range(20):
+        ref.step(r, hq)
+    assert int(p.shortage) == 0
+    _counts_match(p)
+    p.rollback(torch.zeros_like(p.lengths))
+    assert int(p.pool.refs.abs().sum()) == 0
+
+
+def test_chunk_below_a_fork():
+    """The same for a chunk of tokens."""
+    r = np.random.default_rng(1)
+    p = B.PagedKVCache(2, 4, 2, n_pages=20, max_tokens=96, page=16)
+    ref = Histories(p, 96)
+    k, v = _rand(r, 2, 2, 40, 128), _rand(r, 2, 2, 40, 128)
+    p.prefill_chunk(_rand(r, 2, 40, 4, 128), k, v)
+    ref.append(k, v)
+    p.fork(_gpu([0, 0]))
+    ref.fork([0, 0])
+    p.rollback(_gpu([20, 21]))
+    ref.n = [20, 21]
+    k, v = _rand(r, 2, 2, 33, 128), _rand(r, 2, 2, 33, 128)
+    p.prefill_chunk(_rand(r, 2, 33, 4, 128), k, v)
+    ref.append(k, v)
+    ref.step(r, 4)
+    _counts_match(p)
