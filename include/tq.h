@@ -499,7 +499,12 @@ size_t tq_pages_workspace(const tq_page_pool* pool, int rows);
  * they start in the middle of a page that other entries hold too (a row cut
  * back to less than what it was forked with), the row takes a free page in its
  * place as well, with a copy of the contents (with none free its entry is -1:
- * the tokens in that page are lost to the row). */
+ * the tokens in that page are lost to the row). A free page taken for the middle
+ * of which the row's own tokens should be the first part (they were lost, or
+ * given back) has those cleared to zero vectors, which queries see; a row that
+ * is to go on without them is cut back to the page's start first. granted tells
+ * how many of the row's add tokens have a page: those up to the first that has
+ * none. A row whose length grows by that, and not by add, loses nothing else. */
 typedef struct {
     tq_page_pool pool;
     tq_page_table table;
@@ -507,6 +512,7 @@ typedef struct {
     const int32_t* add;     /* device int32 [rows], or NULL: add_all each      */
     int add_all;
     int32_t* shortage;      /* device int32 [1] or NULL                        */
+    int32_t* granted;       /* device int32 [rows] or NULL; not lengths or add */
 } tq_pages_reserve_args;
 tq_status tq_pages_reserve(const tq_pages_reserve_args* a, void* workspace, size_t ws_bytes, tq_stream stream);
 
@@ -533,7 +539,8 @@ tq_status tq_pages_trim(const tq_pages_trim_args* a, tq_stream stream);
  * back); dst and src do not overlap; dst.max_pages >= src.max_pages.
  * A row that is cut back into a page it shares gets its own copy from the next
  * tq_pages_reserve, which comes before its next token. A child whose copy
- * finds no free page keeps its length, and its last tokens are not visible. */
+ * finds no free page keeps its length, and its last tokens are not visible:
+ * its length is best cut back to the page's start (see tq_pages_reserve). */
 typedef struct {
     tq_page_pool pool;
     tq_page_table src, dst;

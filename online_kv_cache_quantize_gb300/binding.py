@@ -107,7 +107,8 @@ class tq_page_table(ctypes.Structure):
 
 class tq_pages_reserve_args(ctypes.Structure):
     _fields_ = [("pool", tq_page_pool), ("table", tq_page_table), ("lengths", ctypes.c_void_p),
-                ("add", ctypes.c_void_p), ("add_all", ctypes.c_int), ("shortage", ctypes.c_void_p)]
+                ("add", ctypes.c_void_p), ("add_all", ctypes.c_int), ("shortage", ctypes.c_void_p),
+                ("granted", ctypes.c_void_p)]
 
 
 class tq_pages_trim_args(ctypes.Structure):
@@ -727,17 +728,19 @@ def tq_pages_workspace(pool, rows):
 
 
 @_bindable("tq_pages_reserve")
-def tq_pages_reserve(pool, table, lengths, add, workspace, shortage=None):
+def tq_pages_reserve(pool, table, lengths, add, workspace, shortage=None, granted=None):
     """Pages for the `add` tokens (an int, or device int32 per row) behind each
     row's lengths[b] tokens; a half-filled last page that other rows hold too is
-    replaced by a copy."""
+    replaced by a copy. granted (device int32 per row): how many of these tokens
+    lie in pages the row holds, from the first on."""
     a = tq_pages_reserve_args(pool.struct(), _table_struct(table), _int32_ptr(lengths, "lengths", table.shape[0]))
     if isinstance(add, int):
         a.add_all = add
     else:
         a.add = _int32_ptr(add, "add", table.shape[0])
     a.shortage = _int32_ptr(shortage, "shortage", 1)
-    return BoundCall("tq_pages_reserve", a, workspace, (pool, table, lengths, add, shortage))
+    a.granted = _int32_ptr(granted, "granted", table.shape[0])
+    return BoundCall("tq_pages_reserve", a, workspace, (pool, table, lengths, add, shortage, granted))
 
 
 @_bindable("tq_pages_trim")
@@ -964,7 +967,8 @@ class PagedKVCache:
     live pages together. Keys are PROD, values MSE. Lengths, tables and counts
     live on the device: no call waits for the GPU. `shortage` counts, on the
     device, the pages that calls asked for and did not get; a caller that sizes
-    the pool for its rows never sees any.
+    the pool for its rows never sees any. A token without a page is lost: its row
+    does not grow by it, and goes on behind the tokens it has (`lengths`).
 
     All calls but `fork` may be captured in a graph (after one run outside, so
     that the workspace is there). How often it is replayed the object cannot
@@ -991,6 +995,7 @@ class PagedKVCache:
         self.lengths = torch.zeros(batch, dtype=torch.int32, device=device)
         self.shortage = torch.zeros(1, dtype=torch.int32, device=device)
         self._short = torch.zeros(1, dtype=torch.int32, device=device)
+        self._granted = torch.zeros(batch, dtype=torch.int32, device=device)  # tokens of the call that have a page
         self._bound = 0  # no row is longer
         self._pages_ws = workspace(tq_pages_workspace(self.pool, batch), device=device)
         self._ws = None
@@ -1013,7 +1018,8 @@ class PagedKVCache:
             self._bound = self.max_tokens
         elif self._bound + add > self.max_tokens:
             raise ValueError("the tokens do not fit max_tokens (after replays, rollback's at_most says what is there)")
-        tq_pages_reserve(self.pool, self.table, self.lengths, add, self._pages_ws, shortage=self._short, stream=stream)
+        tq_pages_reserve(self.pool, self.table, self.lengths, add, self._pages_ws, shortage=self._short,
+                         granted=self._granted, stream=stream)
         with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
             self.shortage += self._short
 
@@ -1021,7 +1027,7 @@ class PagedKVCache:
         import torch
 
         with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
-            self.lengths += add
+            self.lengths += self._granted
         self._bound = min(self._bound + add, self.max_tokens)
         if self.window > 0:
             tq_pages_trim(self.pool, self.table, self.lengths, self.window, self.sinks, stream=stream)
@@ -1051,11 +1057,12 @@ class PagedKVCache:
         with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
             if out is None:
                 out = torch.empty((b, c, self.hq, d), dtype=torch.float32, device=q.device)
-            t = self.lengths.long()[:, None] + torch.arange(c, device=k.device)
-            e = self.table.long().gather(1, (t // self.page).clamp(max=self.max_pages - 1))
-            e = torch.where(t < self.max_tokens, e, -1)[:, None, :]
+            i = torch.arange(c, device=k.device)
+            t = self.lengths.long()[:, None] + i
+            e = self.table.long().gather(1, (t // self.page).clamp(max=self.max_pages - 1))[:, None, :]
             heads = torch.arange(h, device=k.device)[None, :, None]
-            slots = torch.where(e >= 0, (e * h + heads) * self.page + (t % self.page)[:, None, :], -1).reshape(-1)
+            slots = torch.where((i < self._granted[:, None])[:, None, :],
+                                (e * h + heads) * self.page + (t % self.page)[:, None, :], -1).reshape(-1)
             kr, vr = k.reshape(-1, d), v.reshape(-1, d)
         tq_quantize_kv(self.k, self.rot, kr, qjl=self.qjl, dst_slot=slots, stream=stream)
         tq_quantize_kv(self.v, self.rot, vr, dst_slot=slots, stream=stream)
@@ -1078,7 +1085,7 @@ class PagedKVCache:
                 out = torch.empty((self.batch, self.hq, self.d), dtype=torch.float32, device=q.device)
             kn = k_new.reshape(self.batch * self.hkv, self.d)
             vn = v_new.reshape(self.batch * self.hkv, self.d)
-            new_lens = self.lengths + 1
+            new_lens = self.lengths + self._granted
         a = (q, self.k, self.v, new_lens, min(self._bound + 1, self.max_tokens), self.rot, self.qjl, out, kn, vn,
              self.lengths)
         view = self._view()
@@ -1086,6 +1093,11 @@ class PagedKVCache:
         tq_decode_step_view(*a, ws, view, stream=stream)
         self._advance(1, stream)
         return out
+
+    def _cut_lost(self, table, lengths):
+        """Rows whose half-filled last page holds nothing end where it starts."""
+        at = (lengths // self.page).clamp(max=self.max_pages - 1).long()
+        lengths -= (lengths % self.page) * (table.gather(1, at[:, None])[:, 0] < 0)
 
     def fork(self, parent, stream=None):
         """Row i goes on from row parent[i] (device int32 [batch]; outside [0,
@@ -1102,6 +1114,7 @@ class PagedKVCache:
                       keep_src=False, shortage=self._short, stream=stream)
         with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
             self.shortage += self._short
+            self._cut_lost(self._spare, lengths)  # children that found no page for their copy
         self.table, self._spare, self.lengths = self._spare, self.table, lengths
 
     def rollback(self, lengths, at_most=None, stream=None):

@@ -299,9 +299,14 @@ __device__ __forceinline__ int64_t row_tokens(int n, const TableParams& t, int p
 
 // the pages [j0, j1) that the tokens length .. length + add - 1 of a row lie
 // in, and how many of them lie past the table
-__device__ __forceinline__ void reserve_range(const ReserveParams& p, int row, int* j0, int* j1, int* past) {
+__device__ __forceinline__ void reserve_range(const ReserveParams& p, int row, int* j0, int* j1, int* past, int64_t* len = nullptr,
+                                              int64_t* end = nullptr) {
     const int64_t n = max(p.lengths[row], 0);
     const int64_t m = n + max(p.add ? p.add[row] : p.add_all, 0);
+    if (len) {
+        *len = n;
+        *end = m;
+    }
     const int64_t a = n / p.pool.page, b = m > n ? (m + p.pool.page - 1) / p.pool.page : a;
     *j0 = (int)min(a, (int64_t)p.t.max_pages);
     *j1 = (int)min(b, (int64_t)p.t.max_pages);
@@ -333,26 +338,47 @@ __global__ void __launch_bounds__(kPageThreads) reserve_count_kernel(const __gri
     if (lane == 0) p.need[row] = 2 * n + (own ? 1 : 0);
 }
 
+// The first `tokens` tokens of page `pg` become zero vectors: their norms are 0
+// (the planes of 2 bytes a slot), which nothing else of a slot outlives.
+__device__ __forceinline__ void clear_tokens(const PoolParams& pool, int64_t pg, int tokens) {
+    const int slots = pool.slots;
+#pragma unroll
+    for (int q = 0; q < kPagePlanes; ++q) {
+        if (pool.units[q] * 16 != 2 * slots) continue;
+        uint16_t* x = reinterpret_cast<uint16_t*>(pool.base[q]) + pg * slots;
+        for (int i = threadIdx.x; i < slots; i += kPageThreads)
+            if (i % pool.page < tokens) x[i] = 0;
+    }
+}
+
 // One CTA per row. A half-filled last page that another entry holds too is
 // copied to the page the row takes for it (all of the row's holders decide by
 // the counts as they stood, so where all of them take one the old page is free
-// after the call).
+// after the call); one that the row does not hold is cleared up to the row's
+// length, since whatever the page held before would be seen there.
 __global__ void __launch_bounds__(kPageThreads) reserve_take_kernel(const __grid_constant__ ReserveParams p) {
     extern __shared__ int s_pre[];
-    __shared__ int s_from, s_to;
+    __shared__ int s_from, s_to, s_gap;
     wait_prior_grid();
     const int row = blockIdx.x;
     int j0, j1, past;
-    reserve_range(p, row, &j0, &j1, &past);
+    int64_t len, end;
+    reserve_range(p, row, &j0, &j1, &past, &len, &end);
     const int want = p.need[row] >> 1;
     const bool own = p.need[row] & 1;
-    if (threadIdx.x == 0 && past > 0 && p.shortage) atomicAdd(p.shortage, past);
+    if (threadIdx.x == 0) {
+        if (past > 0 && p.shortage) atomicAdd(p.shortage, past);
+        s_from = s_to = -1;
+        s_gap = j1;  // the first page the row does not hold after the call
+        if (want == 0 && p.granted) p.granted[row] = (int)max((int64_t)0, min(end, (int64_t)j1 * p.pool.page) - len);
+    }
     if (want == 0) return;
     load_prefix(p.ix, s_pre);
     int before = 0;
     for (int r = threadIdx.x; r < row; r += kPageThreads) before += p.need[r] >> 1;
     int rank = block_sum(before);  // this row's first request
     const int free_pages = s_pre[p.ix.segs];
+    const int part = (int)(len % p.pool.page);
     for (int j = j0; j < j1; j += kPageThreads) {
         const int jj = j + (int)threadIdx.x;
         int32_t* e = p.t.e + row * p.t.stride + jj;
@@ -366,23 +392,27 @@ __global__ void __launch_bounds__(kPageThreads) reserve_take_kernel(const __grid
             if (r < free_pages) {
                 got = find_free(p.ix, s_pre, r);
                 p.pool.refs[got] = 1;
-            } else if (p.shortage) {
-                atomicAdd(p.shortage, 1);
+            } else {
+                atomicMin(&s_gap, jj);
+                if (p.shortage) atomicAdd(p.shortage, 1);
             }
             *e = got;
-            if (copy) {
-                s_from = old;
+            if (jj == j0 && part) {
+                if (copy) s_from = old;
                 s_to = got;
             }
         }
         rank += total;
     }
-    if (!own) return;
     __syncthreads();
+    if (threadIdx.x == 0 && p.granted) p.granted[row] = (int)max((int64_t)0, min(end, (int64_t)s_gap * p.pool.page) - len);
     const int from = s_from, to = s_to;
-    if (to >= 0)
-        for (int c = 0; c * kCopyUnits < p.pool.off[kPagePlanes]; ++c) copy_chunk(p.pool, p.pool, from, to, c);
-    if (threadIdx.x == 0) atomicSub(p.pool.refs + from, 1);
+    if (to >= 0) {
+        if (from < 0) clear_tokens(p.pool, to, part);
+        else
+            for (int c = 0; c * kCopyUnits < p.pool.off[kPagePlanes]; ++c) copy_chunk(p.pool, p.pool, from, to, c);
+    }
+    if (from >= 0 && threadIdx.x == 0) atomicSub(p.pool.refs + from, 1);
 }
 
 // ------------------------------------------------------------------- fork ---

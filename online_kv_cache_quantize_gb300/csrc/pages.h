@@ -21,7 +21,8 @@ struct PoolParams {
     int off[kPagePlanes + 1];
     int32_t* refs;
     int n_pages;
-    int page;  // tokens
+    int page;   // tokens
+    int slots;  // of a page: tokens x KV heads
 };
 
 struct TableParams {
@@ -49,6 +50,7 @@ struct ReserveParams {
     int add_all;
     int32_t* need;       // [rows] twice a row's requests, + 1 where the first is for a copy of its last page
     int32_t* shortage;   // may be NULL
+    int32_t* granted;    // [rows], may be NULL
 };
 
 struct ForkParams {

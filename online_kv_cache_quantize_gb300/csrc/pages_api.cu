@@ -88,6 +88,7 @@ tq_status pool_params(const tq_page_pool& pool, const std::string& w, tqk::PoolP
     p->refs = pool.refs;
     p->n_pages = pool.n_pages;
     p->page = (int)page;
+    p->slots = (int)(page * pool.hkv);
     return TQ_OK;
 }
 
@@ -197,6 +198,11 @@ tq_status tq_pages_reserve(const tq_pages_reserve_args* a, void* workspace, size
         if ((s = ints(a->lengths, p.t.rows == 0, "tq_pages_reserve: lengths")) != TQ_OK) return s;
         if ((s = ints(a->add, true, "tq_pages_reserve: add")) != TQ_OK) return s;
         if ((s = ints(a->shortage, true, "tq_pages_reserve: shortage")) != TQ_OK) return s;
+        if ((s = ints(a->granted, true, "tq_pages_reserve: granted")) != TQ_OK) return s;
+        // every row reads its length and number after other rows have written theirs
+        if (a->granted && (ranges_meet(a->granted, (size_t)p.t.rows * 4, a->lengths, (size_t)p.t.rows * 4) ||
+                           (a->add && ranges_meet(a->granted, (size_t)p.t.rows * 4, a->add, (size_t)p.t.rows * 4))))
+            return fail(TQ_ERR_INVALID_ARG, "tq_pages_reserve: granted overlaps lengths or add");
         if (!a->add && a->add_all < 0) return fail(TQ_ERR_INVALID_ARG, "tq_pages_reserve: add_all must be >= 0");
         const PagePlan pl = page_plan(a->pool.n_pages, p.t.rows);
         if ((s = check_ws(pl, workspace, ws_bytes, w)) != TQ_OK) return s;
@@ -208,6 +214,7 @@ tq_status tq_pages_reserve(const tq_pages_reserve_args* a, void* workspace, size
         p.add_all = a->add_all;
         p.need = (int32_t*)((char*)workspace + pl.off_row);
         p.shortage = a->shortage;
+        p.granted = a->granted;
         return cuda_status(tqk::launch_pages_reserve(p, (cudaStream_t)stream), w);
     });
 }

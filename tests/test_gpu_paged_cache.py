@@ -165,3 +165,111 @@ def test_chunk_below_a_fork():
     ref.append(k, v)
     ref.step(r, 4)
     _counts_match(p)
+
+
+# --------------------------------------------------- more tokens than pages ---
+def _lossy_step(p, ref, r, hq, stored):
+    """A step of which row b keeps its token where stored[b] == 1."""
+    q, k, v = _rand(r, len(ref.n), hq, 128), _rand(r, len(ref.n), p.hkv, 128), _rand(r, len(ref.n), p.hkv, 128)
+    out = p.step(q, k, v)
+    ref.append(k[:, :, None], v[:, :, None], stored)
+    assert p.lengths.tolist() == ref.n
+    err = float((out - ref.attend(q)).abs().max())
+    assert err <= TOL, err
+
+
+@pytest.mark.parametrize("window", [0, 40])
+def test_steps_without_a_free_page(window):
+    """Tokens that found no page are lost, counted, and never replaced by what a page held before: once there are
+    pages again, the rows go on behind the tokens they have."""
+    r = np.random.default_rng(3)
+    p = B.PagedKVCache(3, 4, 2, n_pages=7, max_tokens=160, page=16, window=window)
+    ref = Histories(p, 160)
+    k, v = _rand(r, 3, 2, 30, 128), _rand(r, 3, 2, 30, 128)
+    p.prefill_chunk(_rand(r, 3, 30, 4, 128), k, v)
+    ref.append(k, v)
+    for _ in range(2):
+        _lossy_step(p, ref, r, 4, [1, 1, 1])
+    assert int(p.shortage) == 0
+    for i in range(3):  # one page for three rows
+        _lossy_step(p, ref, r, 4, [1, 0, 0])
+        assert int(p.shortage) == 2 * (i + 1)
+    p.rollback(_gpu([0, 500, 500]))  # three pages with another row's tokens
+    ref.n[0] = 0
+    for _ in range(12):
+        _lossy_step(p, ref, r, 4, [1, 1, 1])
+    assert int(p.shortage) == 6
+    _counts_match(p)
+
+
+def test_chunk_without_enough_pages():
+    """A chunk of which only the first tokens find pages keeps those."""
+    r = np.random.default_rng(4)
+    p = B.PagedKVCache(3, 4, 2, n_pages=7, max_tokens=160, page=16)
+    ref = Histories(p, 160)
+    for c, stored in ((10, [10, 10, 10]), (50, [50, 22, 6]), (5, [4, 0, 0])):
+        k, v = _rand(r, 3, 2, c, 128), _rand(r, 3, 2, c, 128)
+        p.prefill_chunk(_rand(r, 3, c, 4, 128), k, v)
+        ref.append(k, v, stored)
+        assert p.lengths.tolist() == ref.n
+    p.rollback(_gpu([0, 500, 500]))
+    ref.n[0] = 0
+    for _ in range(9):
+        _lossy_step(p, ref, r, 4, [1, 1, 1])
+    _counts_match(p)
+
+
+def test_fork_without_a_free_page():
+    """Children whose copy of the half-filled page found no page go on from the page's start."""
+    r = np.random.default_rng(5)
+    p = B.PagedKVCache(4, 4, 2, n_pages=14, max_tokens=96, page=16)
+    ref = Histories(p, 96)
+    k, v = _rand(r, 4, 2, 42, 128), _rand(r, 4, 2, 42, 128)
+    p.prefill_chunk(_rand(r, 4, 42, 4, 128), k, v)  # 12 of 14 pages
+    ref.append(k, v)
+    p.fork(_gpu([2, 2, 2, 2]))  # three copies, two pages
+    assert int(p.shortage) == 1
+    ref.fork([2, 2, 2, 2])
+    ref.n = [42, 42, 42, 32]
+    assert p.lengths.tolist() == ref.n
+    for _ in range(9):
+        _lossy_step(p, ref, r, 4, [1, 1, 1, 1])
+    assert int(p.shortage) == 1
+    _counts_match(p)
+
+
+def test_a_page_taken_for_lost_tokens_is_cleared():
+    """An entry filled in the middle of its page: the tokens before are zero vectors, not what the page held."""
+    for mode in ("prod", "polar"):
+        pool = _pool(6, hkv=2, page=32, seed=6, mode=mode)
+        table = _gpu([[0, -1], [-1, -1], [-1, 9]])
+        pool.refs[0] = 1
+        before = _contents(pool)
+        granted = _gpu([7] * 3)
+        B.tq_pages_reserve(pool, table, _gpu([45, 5, 64]), _gpu([20, 2, 3]), _ws(pool, 3), granted=granted)
+        assert table.tolist() == [[0, 1], [2, -1], [-1, 9]]
+        assert granted.tolist() == [19, 2, 0]
+        planes = [pool.k.norm, pool.k.rnorm, pool.v.norm] if mode == "prod" else [pool.k.norm, pool.v.norm]
+        for x in planes:
+            x = x.view(6, 2, 32)
+            assert torch.all(x[1, :, :13] == 0) and torch.all(x[2, :, :5] == 0)
+            x[1, :, :13] = x[2, :, :5] = 1
+        want = torch.from_numpy(before)
+        got = torch.from_numpy(_contents(pool))
+        same = (want == got).all(dim=1)
+        assert same.tolist() == [True, False, False, True, True, True]
+        # nothing else of the two pages changed
+        assert int((want != got).sum()) <= len(planes) * 2 * 2 * (13 + 5)
+
+
+def test_granted_tokens():
+    """granted is the row's tokens that lie in pages it holds, from the first on."""
+    pool = _pool(5, hkv=1, page=16)
+    table = _gpu([[0, -1, -1], [-1, -1, 1], [2, -1, -1], [-1, -1, -1]])
+    pool.refs[:3] = 1
+    granted = _gpu([9] * 4)
+    add = _gpu([40, 48, 6, 0])
+    B.tq_pages_reserve(pool, table, _gpu([10, -3, 16, 5]), add, _ws(pool, 4), granted=granted)
+    # free: 3, 4. Row 0 takes both (tokens 10 .. 47 of 10 .. 49); rows 1 and 2 find none
+    assert table.tolist() == [[0, 3, 4], [-1, -1, 1], [2, -1, -1], [-1, -1, -1]]
+    assert granted.tolist() == [38, 0, 0, 0]
