@@ -991,7 +991,7 @@ class PagedKVCache:
         self.v = Cache("mse", v_bits, d, rows=n_pages * hkv, capacity=page, device=device, bits2=v_bits2)
         self.pool = PagePool(self.k, self.v, hkv)
         self.table = self.pool.table(batch, self.max_pages)
-        self._spare = self.pool.table(batch, self.max_pages)
+        self._spare = self.pool.table(batch, self.max_pages)  # where a fork forms its rows; what it held is not counted
         self.lengths = torch.zeros(batch, dtype=torch.int32, device=device)
         self.shortage = torch.zeros(1, dtype=torch.int32, device=device)
         self._short = torch.zeros(1, dtype=torch.int32, device=device)
@@ -1101,9 +1101,9 @@ class PagedKVCache:
 
     def fork(self, parent, stream=None):
         """Row i goes on from row parent[i] (device int32 [batch]; outside [0,
-        batch): an empty row). Rows without a child are freed. Not captured:
-        it exchanges the table and the lengths for others (tq_pages_fork on a
-        caller's own tables can be)."""
+        batch): an empty row). Rows without a child are freed. The table and the
+        lengths stay where they are, so that graphs captured before go on from
+        them. Not captured itself (tq_pages_fork on a caller's own tables can be)."""
         import torch
 
         if self._capturing(stream):
@@ -1115,7 +1115,8 @@ class PagedKVCache:
         with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
             self.shortage += self._short
             self._cut_lost(self._spare, lengths)  # children that found no page for their copy
-        self.table, self._spare, self.lengths = self._spare, self.table, lengths
+            self.table.copy_(self._spare)
+            self.lengths.copy_(lengths)
 
     def rollback(self, lengths, at_most=None, stream=None):
         """Drops the tokens behind the first lengths[b] of every row (device

@@ -273,3 +273,85 @@ def test_granted_tokens():
     # free: 3, 4. Row 0 takes both (tokens 10 .. 47 of 10 .. 49); rows 1 and 2 find none
     assert table.tolist() == [[0, 3, 4], [-1, -1, 1], [2, -1, -1], [-1, -1, -1]]
     assert granted.tolist() == [38, 0, 0, 0]
+
+
+# -------------------------------------------------- captured calls and others ---
+def _captured(p, r, hq):
+    """A step captured with inputs of its own, and a function that replays it with new ones on both sides."""
+    bufs = [_rand(r, p.batch, hq, 128), _rand(r, p.batch, p.hkv, 128), _rand(r, p.batch, p.hkv, 128)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = p.step(*bufs)
+
+    def replay(ref):
+        for b in bufs:
+            b.copy_(_rand(r, *b.shape))
+        g.replay()
+        ref.append(bufs[1][:, :, None], bufs[2][:, :, None])
+        err = float((out - ref.attend(bufs[0])).abs().max())
+        assert err <= TOL, err
+        assert p.lengths.tolist() == ref.n
+
+    return replay
+
+
+def test_a_fork_between_replays():
+    """A captured step goes on from what a fork, a rollback and a compaction made of the rows since."""
+    r = np.random.default_rng(6)
+    p = B.PagedKVCache(3, 4, 2, n_pages=30, max_tokens=128, page=16)
+    ref = Histories(p, 128)
+    k, v = _rand(r, 3, 2, 20, 128), _rand(r, 3, 2, 20, 128)
+    p.prefill_chunk(_rand(r, 3, 20, 4, 128), k, v)
+    ref.append(k, v)
+    ref.step(r, 4)
+    replay = _captured(p, r, 4)
+    replay(ref)
+    for parent in ([2, 2, 0], [1, 0, 0], [0, 1, 2]):
+        p.fork(_gpu(parent))
+        ref.fork(parent)
+        for _ in range(9):
+            replay(ref)
+        p.compact()
+    p.rollback(_gpu([30, 40, 8]))
+    ref.n = [30, 40, 8]
+    for _ in range(5):
+        replay(ref)
+    _counts_match(p)
+
+
+def test_calls_on_a_stream_of_their_own():
+    """Every call on a side stream that is behind, while the stream of the constructor takes and gives back
+    memory: nothing that the queued work still reads may have moved or gone."""
+    r = np.random.default_rng(9)
+    p = B.PagedKVCache(2, 4, 2, n_pages=24, max_tokens=128, page=16)
+    ref = Histories(p, 128)
+    at = (p.table.data_ptr(), p.lengths.data_ptr())
+    xs = [(_rand(r, 2, 4, 128), _rand(r, 2, 2, 128), _rand(r, 2, 2, 128)) for _ in range(20)]
+    k, v = _rand(r, 2, 2, 30, 128), _rand(r, 2, 2, 30, 128)
+    q = _rand(r, 2, 30, 4, 128)
+    forks = [_gpu([1, 1]), _gpu([1, 0])]
+    back = _gpu([33, 20])
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    outs = []
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(200_000_000)  # about 0.1 s
+    p.prefill_chunk(q, k, v, stream=s)
+    for i, x in enumerate(xs):
+        outs.append(p.step(*x, stream=s))
+        if i in (4, 12):
+            p.fork(forks[i == 12], stream=s)
+        if i == 8:
+            p.rollback(back, stream=s)
+        junk = [torch.full((n,), 0x7FFFFFFF, dtype=torch.int32, device="cuda") for n in (2, 2, 16, 16, 512)]
+        del junk
+    s.synchronize()
+    ref.append(k, v)
+    for i, x in enumerate(xs):
+        ref.append(x[1][:, :, None], x[2][:, :, None])
+        assert float((outs[i] - ref.attend(x[0])).abs().max()) <= TOL, i
+        if i in (4, 12):
+            ref.fork(forks[i == 12].tolist())
+        if i == 8:
+            ref.n = [33, 20]
+    assert p.lengths.tolist() == ref.n and at == (p.table.data_ptr(), p.lengths.data_ptr())
