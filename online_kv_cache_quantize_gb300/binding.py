@@ -972,8 +972,9 @@ class PagedKVCache:
 
     All calls but `fork` may be captured in a graph (after one run outside, so
     that the workspace is there). How often it is replayed the object cannot
-    know: captured calls plan for max_tokens, tokens past it are dropped, and
-    calls made outside afterwards need a `rollback` with at_most first."""
+    know: from the first capture on, every call plans for max_tokens, tokens past
+    it are dropped, and calls made outside afterwards need a `rollback` with
+    at_most first."""
 
     def __init__(self, batch, hq, hkv, n_pages, max_tokens, page=64, d=128, k_bits=3, v_bits=3, window=0, sinks=0,
                  rotation="rht", rot_seed=1, qjl_seed=2, device="cuda", k_bits2=None, v_bits2=None):
@@ -996,7 +997,8 @@ class PagedKVCache:
         self.shortage = torch.zeros(1, dtype=torch.int32, device=device)
         self._short = torch.zeros(1, dtype=torch.int32, device=device)
         self._granted = torch.zeros(batch, dtype=torch.int32, device=device)  # tokens of the call that have a page
-        self._bound = 0  # no row is longer
+        self._bound = 0  # no row is longer, but for replays
+        self._replays = False  # a call that appends was captured
         self._pages_ws = workspace(tq_pages_workspace(self.pool, batch), device=device)
         self._ws = None
         self._captured = []  # workspaces that graphs hold the addresses of
@@ -1015,13 +1017,17 @@ class PagedKVCache:
         import torch
 
         if self._capturing(stream):
-            self._bound = self.max_tokens
+            self._bound, self._replays = self.max_tokens, True
         elif self._bound + add > self.max_tokens:
             raise ValueError("the tokens do not fit max_tokens (after replays, rollback's at_most says what is there)")
         tq_pages_reserve(self.pool, self.table, self.lengths, add, self._pages_ws, shortage=self._short,
                          granted=self._granted, stream=stream)
         with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
             self.shortage += self._short
+
+    def _longest(self, add):
+        """No row is longer with `add` more tokens."""
+        return self.max_tokens if self._replays else min(self._bound + add, self.max_tokens)
 
     def _advance(self, add, stream):
         import torch
@@ -1066,7 +1072,7 @@ class PagedKVCache:
             kr, vr = k.reshape(-1, d), v.reshape(-1, d)
         tq_quantize_kv(self.k, self.rot, kr, qjl=self.qjl, dst_slot=slots, stream=stream)
         tq_quantize_kv(self.v, self.rot, vr, dst_slot=slots, stream=stream)
-        a = (q, self.k, self.v, self.lengths, min(self._bound + c, self.max_tokens), self.rot, self.qjl, out)
+        a = (q, self.k, self.v, self.lengths, self._longest(c), self.rot, self.qjl, out)
         view = self._view()
         ws = self._workspace(tq_attn_prefill_view_workspace(*a, view), stream)
         tq_attn_prefill_view(*a, ws, view, stream=stream)
@@ -1086,7 +1092,7 @@ class PagedKVCache:
             kn = k_new.reshape(self.batch * self.hkv, self.d)
             vn = v_new.reshape(self.batch * self.hkv, self.d)
             new_lens = self.lengths + self._granted
-        a = (q, self.k, self.v, new_lens, min(self._bound + 1, self.max_tokens), self.rot, self.qjl, out, kn, vn,
+        a = (q, self.k, self.v, new_lens, self._longest(1), self.rot, self.qjl, out, kn, vn,
              self.lengths)
         view = self._view()
         ws = self._workspace(tq_decode_step_view_workspace(*a, view), stream)
@@ -1132,7 +1138,8 @@ class PagedKVCache:
         _int32_ptr(lengths, "lengths", self.batch)
         if at_most is not None:
             at_most = max(int(at_most), 0)
-            self._bound = min(self._bound, at_most)
+            if not self._capturing(stream):  # else nothing has run yet
+                self._bound = min(self._bound, at_most)
         with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
             self.lengths.copy_(torch.minimum(self.lengths, lengths.clamp(min=0, max=at_most)))
         tq_pages_trim(self.pool, self.table, self.lengths, self.window, self.sinks, stream=stream)

@@ -355,3 +355,41 @@ def test_calls_on_a_stream_of_their_own():
         if i == 8:
             ref.n = [33, 20]
     assert p.lengths.tolist() == ref.n and at == (p.table.data_ptr(), p.lengths.data_ptr())
+
+
+def test_steps_outside_after_replays():
+    """rollback's at_most says how long the rows are then; replays make them longer, and a step outside sees it."""
+    r = np.random.default_rng(7)
+    p = B.PagedKVCache(2, 4, 2, n_pages=20, max_tokens=128, page=16)
+    ref = Histories(p, 128)
+    ref.step(r, 4)
+    replay = _captured(p, r, 4)
+    for _ in range(30):
+        replay(ref)
+    p.rollback(_gpu([25, 11]), at_most=25)
+    ref.n = [25, 11]
+    ref.step(r, 4)
+    for _ in range(40):
+        replay(ref)
+    ref.step(r, 4)
+    k, v = _rand(r, 2, 2, 5, 128), _rand(r, 2, 2, 5, 128)
+    p.prefill_chunk(_rand(r, 2, 5, 4, 128), k, v)
+    ref.append(k, v)
+    ref.step(r, 4)
+
+
+def test_a_captured_rollback_has_not_run():
+    r = np.random.default_rng(8)
+    p = B.PagedKVCache(2, 4, 2, n_pages=20, max_tokens=128, page=16)
+    ref = Histories(p, 128)
+    for _ in range(20):
+        ref.step(r, 4)
+    to = _gpu([10, 10])
+    p.rollback(_gpu([20, 20]))  # outside first
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        p.rollback(to, at_most=10)
+    ref.step(r, 4)  # 21 tokens
+    g.replay()
+    ref.n = [10, 10]
+    ref.step(r, 4)
