@@ -961,7 +961,9 @@ class PagedKVCache:
     generation loop: `prefill_chunk` and `step` reserve pages, append and
     attend (tq_pages_reserve, tq_quantize_kv, tq_attn_prefill_view,
     tq_decode_step_view) and, with a window, give back the pages it has passed
-    (tq_pages_trim; a page goes once no later query sees it); `fork` makes
+    (tq_pages_trim; a page goes once no later query sees it, nor one after a
+    rollback of up to max_rollback tokens: the longest draft that a speculative
+    decoder may take back); `fork` makes
     every row a child of some row, as beam search and sampling do
     (tq_pages_fork); `rollback` drops tokens or frees rows, `compact` moves the
     live pages together. Keys are PROD, values MSE. Lengths, tables and counts
@@ -977,12 +979,15 @@ class PagedKVCache:
     at_most first."""
 
     def __init__(self, batch, hq, hkv, n_pages, max_tokens, page=64, d=128, k_bits=3, v_bits=3, window=0, sinks=0,
-                 rotation="rht", rot_seed=1, qjl_seed=2, device="cuda", k_bits2=None, v_bits2=None):
+                 rotation="rht", rot_seed=1, qjl_seed=2, device="cuda", k_bits2=None, v_bits2=None, max_rollback=0):
         import torch
 
         if hq % hkv:
             raise ValueError("hq must be a multiple of hkv")
+        if max_rollback < 0:
+            raise ValueError("max_rollback must be >= 0")
         self.batch, self.hq, self.hkv, self.d, self.page = batch, hq, hkv, d, page
+        self.max_rollback = max_rollback
         self.window, self.sinks = window, sinks
         self.max_pages = -(-max_tokens // page)
         self.max_tokens = self.max_pages * page
@@ -1036,7 +1041,12 @@ class PagedKVCache:
             self.lengths += self._granted
         self._bound = min(self._bound + add, self.max_tokens)
         if self.window > 0:
-            tq_pages_trim(self.pool, self.table, self.lengths, self.window, self.sinks, stream=stream)
+            self._trim(stream)
+
+    def _trim(self, stream):
+        """Gives back the pages that no query sees, now or after a rollback."""
+        window = min(self.window + self.max_rollback, 2**31 - 1) if self.window > 0 else 0
+        tq_pages_trim(self.pool, self.table, self.lengths, window, self.sinks, stream=stream)
 
     def _workspace(self, need, stream):
         import torch
@@ -1131,8 +1141,10 @@ class PagedKVCache:
         host how long the rows are where it knows a lower bound than the tokens
         appended so far (the calls plan with it and refuse what would pass
         max_tokens). Rows may go back to less than they were forked with: the
-        page they go on in is copied by the next call that appends. A row whose
-        window has moved on cannot get its old tokens back."""
+        page they go on in is copied by the next call that appends. With a window,
+        a row that goes back by more than max_rollback tokens may find pages of its
+        window gone: they count as shortage, their tokens are not visible, and
+        where the row's last page is among them it goes on from that page's start."""
         import torch
 
         _int32_ptr(lengths, "lengths", self.batch)
@@ -1141,8 +1153,17 @@ class PagedKVCache:
             if not self._capturing(stream):  # else nothing has run yet
                 self._bound = min(self._bound, at_most)
         with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
-            self.lengths.copy_(torch.minimum(self.lengths, lengths.clamp(min=0, max=at_most)))
-        tq_pages_trim(self.pool, self.table, self.lengths, self.window, self.sinks, stream=stream)
+            new = torch.minimum(self.lengths, lengths.clamp(min=0, max=at_most))
+            if self.window > 0:
+                # the pages with tokens of the window or the sinks
+                j = torch.arange(self.max_pages, device=new.device)[None] * self.page
+                n = new[:, None]
+                seen = (j < n) & ((j + self.page > n - self.window) | (j < self.sinks))
+                gone = seen & (self.table < 0) & (n < self.lengths[:, None])
+                self.shortage += gone.sum().int()
+                self._cut_lost(self.table, new)
+            self.lengths.copy_(new)
+        self._trim(stream)
 
     def compact(self, stream=None):
         """Moves the live pages to the lowest page numbers of the pool."""

@@ -393,3 +393,44 @@ def test_a_captured_rollback_has_not_run():
     g.replay()
     ref.n = [10, 10]
     ref.step(r, 4)
+
+
+# -------------------------------------------------------- windowed rollback ---
+@pytest.mark.parametrize("window,sinks,keep", [(20, 0, 24), (33, 5, 16), (16, 20, 40), (1, 0, 8)])
+def test_windowed_rollback_keeps_what_the_window_reaches(window, sinks, keep):
+    """Drafts of up to max_rollback tokens, of which some are dropped: every query sees all tokens of its window."""
+    r = np.random.default_rng(window)
+    p = B.PagedKVCache(2, 4, 2, n_pages=2 * (5 + (window + keep) // 16), max_tokens=512, page=16, window=window, sinks=sinks,
+                       max_rollback=keep)
+    ref = Histories(p, 512)
+    for _ in range(12):
+        c = int(r.integers(1, keep + 1))
+        k, v = _rand(r, 2, 2, c, 128), _rand(r, 2, 2, c, 128)
+        p.prefill_chunk(_rand(r, 2, c, 4, 128), k, v)
+        ref.append(k, v)
+        to = [n - int(r.integers(0, c + 1)) for n in ref.n]
+        p.rollback(_gpu(to))
+        ref.n = to
+        ref.step(r, 4)
+    assert int(p.shortage) == 0
+    _counts_match(p)
+
+
+def test_windowed_rollback_past_the_margin_is_counted():
+    """Pages of the new window that are already gone count as shortage; freeing a row does not."""
+    r = np.random.default_rng(2)
+    p = B.PagedKVCache(2, 4, 2, n_pages=20, max_tokens=256, page=16, window=32)
+    ref = Histories(p, 256)
+    k, v = _rand(r, 2, 2, 100, 128), _rand(r, 2, 2, 100, 128)
+    p.prefill_chunk(_rand(r, 2, 100, 4, 128), k, v)  # tokens 64 .. stay
+    ref.append(k, v)
+    p.rollback(_gpu([98, 0]))
+    assert int(p.shortage) == 0 and p.lengths.tolist() == [98, 0]
+    p.rollback(_gpu([70, 0]))  # sees 38 .. 69: pages 2 and 3 are gone
+    assert int(p.shortage) == 2 and p.lengths.tolist() == [70, 0]
+    p.rollback(_gpu([41, 0]))  # the page it would go on in is gone: on from its start
+    assert p.lengths.tolist() == [32, 0]
+    ref.n = [0, 0]
+    p.rollback(_gpu([0, 0]))
+    ref.step(r, 4)
+    _counts_match(p)
