@@ -1053,6 +1053,12 @@ class PagedKVCache:
 
         if self._ws is None or self._ws.numel() < need:
             with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+                if self._ws is not None:
+                    # queued work may still use the one that goes, on another stream than its own
+                    if torch.cuda.is_current_stream_capturing():
+                        self._captured.append(self._ws)
+                    else:
+                        self._ws.record_stream(torch.cuda.current_stream())
                 self._ws = workspace(need, device=self.lengths.device)
         if self._capturing(stream) and not any(w is self._ws for w in self._captured):
             self._captured.append(self._ws)

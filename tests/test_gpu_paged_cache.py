@@ -434,3 +434,28 @@ def test_windowed_rollback_past_the_margin_is_counted():
     p.rollback(_gpu([0, 0]))
     ref.step(r, 4)
     _counts_match(p)
+
+
+def test_a_workspace_that_grows_on_another_stream():
+    """The workspace that a larger call replaces is not given to others while a stream still has work that uses it."""
+    r = np.random.default_rng(10)
+    p = B.PagedKVCache(2, 4, 2, n_pages=40, max_tokens=256, page=16)
+    ref = Histories(p, 256)
+    ref.step(r, 4)  # the workspace belongs to this stream
+    old = p._ws.data_ptr()
+    size = p._ws.numel()
+    x = [_rand(r, 2, 4, 128), _rand(r, 2, 2, 128), _rand(r, 2, 2, 128)]
+    k, v, q = _rand(r, 2, 2, 200, 128), _rand(r, 2, 2, 200, 128), _rand(r, 2, 200, 4, 128)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(400_000_000)
+    out = p.step(*x, stream=s)
+    p.prefill_chunk(q, k, v, stream=s)
+    assert p._ws.data_ptr() != old
+    if not s.query():  # the step has not run yet
+        taken = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(8)]
+        assert all(t.data_ptr() != old for t in taken)
+    s.synchronize()
+    ref.append(x[1][:, :, None], x[2][:, :, None])
+    assert float((out - ref.attend(x[0])).abs().max()) <= TOL
