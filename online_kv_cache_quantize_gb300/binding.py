@@ -562,6 +562,56 @@ def _table_check(t, what):
         raise ValueError(f"{what} must be a 2-D int32 tensor with unit inner stride")
 
 
+def _int_check(x, what):
+    """The C structs hold int32: a larger number would be cut to its low bits."""
+    if not -2**31 <= x < 2**31:
+        raise ValueError(f"{what} must fit 32 bits")
+    return x
+
+
+def _device_check(home, **tensors):
+    """Every tensor of a call lies on the GPU that `home` lies on."""
+    for what, t in tensors.items():
+        if t is not None and t.device != home.device:
+            raise ValueError(f"{what} is on {t.device}, the caches are on {home.device}")
+    if home.device.type != "cuda":
+        raise ValueError("the caches must be on a GPU")
+
+
+def _dense_check(t, what, n, dtypes=None):
+    """A contiguous tensor of n values (the kernels know no strides)."""
+    import torch
+
+    names = dtypes or (torch.float32, torch.bfloat16)
+    if t.dtype not in names:
+        raise ValueError(f"{what} must be of {' or '.join(str(x) for x in names)}")
+    if not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{what} must be contiguous and hold {n} values")
+
+
+def _attend_check(view, kcache, vcache, q, pos, pos_name, out, gqa_map=None, logits=None, max_seq_len=0, rows=None,
+                  **_):
+    """The tensors of a windowed / paged attention call, before their addresses go to the library."""
+    import torch
+
+    batch, hq, d = q.shape[0], q.shape[-2], q.shape[-1]
+    _dense_check(q, "q", q.numel())
+    _dense_check(out, "out", q.numel())
+    _int32_ptr(pos, pos_name, batch)
+    if gqa_map is not None and len(gqa_map) != hq:
+        raise ValueError("gqa_map must have an entry per query head")
+    if logits is not None:
+        _dense_check(logits, "logits", batch * hq * max_seq_len if max_seq_len > 0 else logits.numel(), (torch.float32,))
+    k_new, v_new, append_pos = rows or (None, None, None)
+    if rows:
+        n = batch * view.hkv(kcache, batch) * d
+        _dense_check(k_new, "k_new", n)
+        _dense_check(v_new, "v_new", n, (k_new.dtype,))
+        _int32_ptr(append_pos, "append_pos", batch)
+    _device_check(kcache.codes, vcache=vcache.codes, q=q, out=out, logits=logits, page_table=view.page_table, k_new=k_new,
+                  v_new=v_new, append_pos=append_pos, **{pos_name: pos})
+
+
 class View:
     """What an attention call sees of each sequence (tq_view): window (0: every
     token) and sinks, and, for a paged cache, its page table (device int32
@@ -570,7 +620,9 @@ class View:
     def __init__(self, window=0, sinks=0, page_table=None, n_pages=0):
         if page_table is not None:
             _table_check(page_table, "page_table")
-        self.window, self.sinks, self.page_table, self.n_pages = window, sinks, page_table, n_pages
+        self.window, self.sinks, self.n_pages = (_int_check(x, w) for x, w in ((window, "window"), (sinks, "sinks"),
+                                                                              (n_pages, "n_pages")))
+        self.page_table = page_table
 
     def struct(self):
         t = self.page_table
@@ -597,6 +649,8 @@ class BoundCall:
         self._fn, self._name, self._a, self._keep = getattr(load(), name), name, struct, (workspace, keep)
         self._args = (ctypes.byref(struct),)
         if workspace is not None:
+            if not workspace.is_contiguous():
+                raise ValueError("the workspace must be contiguous")
             self._args += (ctypes.c_void_p(workspace.data_ptr()),
                            ctypes.c_size_t(workspace.numel() * workspace.element_size()))
 
@@ -630,6 +684,7 @@ def prepare(fn, *args, **kw):
 
 
 def _decode_view_struct(q, kcache, vcache, seq_lens, max_seq_len, rot, qjl, out, view, **kw):
+    _attend_check(view, kcache, vcache, q, seq_lens, "seq_lens", out, max_seq_len=max_seq_len, **kw)
     attn, keep = _decode_struct(q, kcache, vcache, seq_lens, max_seq_len, rot, qjl, out,
                                 hkv=view.hkv(kcache, q.shape[0]), **kw)
     return tq_decode_view_args(attn, view.struct()), (keep, q, kcache, vcache, seq_lens, rot, qjl, out, view, kw)
@@ -645,10 +700,13 @@ def tq_attn_decode_view(q, kcache, vcache, seq_lens, max_seq_len, rot, qjl, out,
     """tq_attn_decode over the tokens `view` leaves visible, of contiguous or
     paged caches (a paged cache has n_pages * hkv rows)."""
     a, keep = _decode_view_struct(q, kcache, vcache, seq_lens, max_seq_len, rot, qjl, out, view, **kw)
+    _device_check(kcache.codes, workspace=workspace)
     return BoundCall("tq_attn_decode_view", a, workspace, keep)
 
 
 def _step_view_struct(q, kcache, vcache, seq_lens, max_seq_len, rot, qjl, out, k_new, v_new, append_pos, view, **kw):
+    _attend_check(view, kcache, vcache, q, seq_lens, "seq_lens", out, max_seq_len=max_seq_len,
+                  rows=(k_new, v_new, append_pos), **kw)
     step, keep = _step_struct(q, kcache, vcache, seq_lens, max_seq_len, rot, qjl, out, k_new, v_new, append_pos,
                               hkv=view.hkv(kcache, q.shape[0]), **kw)
     return tq_step_view_args(step, view.struct()), (keep, q, kcache, vcache, seq_lens, rot, qjl, out, k_new, v_new,
@@ -669,10 +727,12 @@ def tq_decode_step_view(q, kcache, vcache, seq_lens, max_seq_len, rot, qjl, out,
     sequence b goes to position append_pos[b] through the page table."""
     a, keep = _step_view_struct(q, kcache, vcache, seq_lens, max_seq_len, rot, qjl, out, k_new, v_new, append_pos,
                                 view, **kw)
+    _device_check(kcache.codes, workspace=workspace)
     return BoundCall("tq_decode_step_view", a, workspace, keep)
 
 
 def _prefill_view_struct(q, kcache, vcache, q_start, max_context, rot, qjl, out, view, **kw):
+    _attend_check(view, kcache, vcache, q, q_start, "q_start", out, **kw)
     attn, keep = _prefill_struct(q, kcache, vcache, q_start, max_context, rot, qjl, out,
                                  hkv=view.hkv(kcache, q.shape[0]), **kw)
     return tq_prefill_view_args(attn, view.struct()), (keep, q, kcache, vcache, q_start, rot, qjl, out, view, kw)
@@ -687,6 +747,7 @@ def tq_attn_prefill_view_workspace(q, kcache, vcache, q_start, max_context, rot,
 def tq_attn_prefill_view(q, kcache, vcache, q_start, max_context, rot, qjl, out, workspace, view, **kw):
     """tq_attn_prefill over the tokens `view` leaves visible to each query."""
     a, keep = _prefill_view_struct(q, kcache, vcache, q_start, max_context, rot, qjl, out, view, **kw)
+    _device_check(kcache.codes, workspace=workspace)
     return BoundCall("tq_attn_prefill_view", a, workspace, keep)
 
 
@@ -705,6 +766,8 @@ class PagePool:
         self.refs = refs if refs is not None else torch.zeros(self.n_pages, dtype=torch.int32,
                                                               device=kcache.codes.device)
         _int32_ptr(self.refs, "refs", self.n_pages)
+        if self.refs.device != kcache.codes.device or vcache.codes.device != kcache.codes.device:
+            raise ValueError("the caches and refs must be on one device")
 
     def table(self, rows, max_pages):
         """An empty page table (every entry -1)."""
@@ -735,11 +798,13 @@ def tq_pages_reserve(pool, table, lengths, add, workspace, shortage=None, grante
     lie in pages the row holds, from the first on."""
     a = tq_pages_reserve_args(pool.struct(), _table_struct(table), _int32_ptr(lengths, "lengths", table.shape[0]))
     if isinstance(add, int):
-        a.add_all = add
+        a.add_all = _int_check(add, "add")
     else:
         a.add = _int32_ptr(add, "add", table.shape[0])
     a.shortage = _int32_ptr(shortage, "shortage", 1)
     a.granted = _int32_ptr(granted, "granted", table.shape[0])
+    _device_check(pool.refs, table=table, lengths=lengths, add=None if isinstance(add, int) else add, shortage=shortage,
+                  granted=granted, workspace=workspace)
     return BoundCall("tq_pages_reserve", a, workspace, (pool, table, lengths, add, shortage, granted))
 
 
@@ -747,8 +812,9 @@ def tq_pages_reserve(pool, table, lengths, add, workspace, shortage=None, grante
 def tq_pages_trim(pool, table, lengths, window=0, sinks=0):
     """Gives back the pages that hold no token a query from position
     lengths[b] - 1 on sees."""
-    a = tq_pages_trim_args(pool.struct(), _table_struct(table), _int32_ptr(lengths, "lengths", table.shape[0]), window,
-                           sinks)
+    a = tq_pages_trim_args(pool.struct(), _table_struct(table), _int32_ptr(lengths, "lengths", table.shape[0]),
+                           _int_check(window, "window"), _int_check(sinks, "sinks"))
+    _device_check(pool.refs, table=table, lengths=lengths)
     return BoundCall("tq_pages_trim", a, None, (pool, table, lengths))
 
 
@@ -761,6 +827,8 @@ def tq_pages_fork(pool, src, dst, parent, src_lengths, dst_lengths, workspace, k
                            _int32_ptr(src_lengths, "src_lengths", src.shape[0]),
                            _int32_ptr(dst_lengths, "dst_lengths", dst.shape[0]), 1 if keep_src else 0,
                            _int32_ptr(shortage, "shortage", 1))
+    _device_check(pool.refs, src=src, dst=dst, parent=parent, src_lengths=src_lengths, dst_lengths=dst_lengths,
+                  shortage=shortage, workspace=workspace)
     return BoundCall("tq_pages_fork", a, workspace,
                      (pool, src, dst, parent, src_lengths, dst_lengths, shortage))
 
@@ -771,6 +839,7 @@ def tq_pages_copy(src_pool, dst_pool, src_pages, dst_pages):
     n = src_pages.numel()
     a = tq_pages_copy_args(src_pool.struct(), dst_pool.struct(), _int32_ptr(src_pages, "src_pages"),
                            _int32_ptr(dst_pages, "dst_pages", n), n)
+    _device_check(src_pool.refs, dst_pool=dst_pool.refs, src_pages=src_pages, dst_pages=dst_pages)
     return BoundCall("tq_pages_copy", a, None, (src_pool, dst_pool, src_pages, dst_pages))
 
 
@@ -788,6 +857,8 @@ def tq_pages_compact(src_pool, src_tables, dst_pool, dst_tables, workspace, live
         a.src_tables[i], a.dst_tables[i] = _table_struct(x), _table_struct(y)
     a.n_tables = len(st)
     a.live = _int32_ptr(live, "live", 1)
+    _device_check(src_pool.refs, dst_pool=dst_pool.refs, live=live, workspace=workspace,
+                  **{f"table {i}": t for i, t in enumerate(st + dt)})
     return BoundCall("tq_pages_compact", a, workspace, (src_pool, st, dst_pool, dt, live))
 
 
@@ -1030,6 +1101,19 @@ class PagedKVCache:
         with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
             self.shortage += self._short
 
+    def _inputs_check(self, q, k, v, out):
+        """Before anything is enqueued; strided inputs are copied."""
+        import torch
+
+        for t, what in ((q, "q"), (k, "the keys"), (v, "the values")):
+            if t.dtype not in (torch.float32, torch.bfloat16):
+                raise ValueError(f"{what} must be float32 or bfloat16")
+        if k.dtype != v.dtype:
+            raise ValueError("keys and values must have the same dtype")
+        if out is not None:
+            _dense_check(out, "out", q.numel())
+        _device_check(self.lengths, q=q, k=k, v=v, out=out)
+
     def _longest(self, add):
         """No row is longer with `add` more tokens."""
         return self.max_tokens if self._replays else min(self._bound + add, self.max_tokens)
@@ -1075,17 +1159,19 @@ class PagedKVCache:
             raise ValueError("k and v must be [batch, hkv, C, d]")
         if tuple(q.shape) != (b, c, self.hq, d):
             raise ValueError("q must be [batch, C, hq, d]")
+        self._inputs_check(q, k, v, out)
         self._reserve(c, stream)
         with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
             if out is None:
                 out = torch.empty((b, c, self.hq, d), dtype=torch.float32, device=q.device)
+            q = q.contiguous()
             i = torch.arange(c, device=k.device)
             t = self.lengths.long()[:, None] + i
             e = self.table.long().gather(1, (t // self.page).clamp(max=self.max_pages - 1))[:, None, :]
             heads = torch.arange(h, device=k.device)[None, :, None]
             slots = torch.where((i < self._granted[:, None])[:, None, :],
                                 (e * h + heads) * self.page + (t % self.page)[:, None, :], -1).reshape(-1)
-            kr, vr = k.reshape(-1, d), v.reshape(-1, d)
+            kr, vr = (x if x.stride(1) == 1 else x.contiguous() for x in (k.reshape(-1, d), v.reshape(-1, d)))
         tq_quantize_kv(self.k, self.rot, kr, qjl=self.qjl, dst_slot=slots, stream=stream)
         tq_quantize_kv(self.v, self.rot, vr, dst_slot=slots, stream=stream)
         a = (q, self.k, self.v, self.lengths, self._longest(c), self.rot, self.qjl, out)
@@ -1101,12 +1187,16 @@ class PagedKVCache:
         fp32 unless given)."""
         import torch
 
+        if tuple(q.shape) != (self.batch, self.hq, self.d):
+            raise ValueError("q must be [batch, hq, d]")
+        if not tuple(k_new.shape) == tuple(v_new.shape) == (self.batch, self.hkv, self.d):
+            raise ValueError("k_new and v_new must be [batch, hkv, d]")
+        self._inputs_check(q, k_new, v_new, out)
         self._reserve(1, stream)
         with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
             if out is None:
                 out = torch.empty((self.batch, self.hq, self.d), dtype=torch.float32, device=q.device)
-            kn = k_new.reshape(self.batch * self.hkv, self.d)
-            vn = v_new.reshape(self.batch * self.hkv, self.d)
+            q, kn, vn = q.contiguous(), k_new.contiguous(), v_new.contiguous()
             new_lens = self.lengths + self._granted
         a = (q, self.k, self.v, new_lens, self._longest(1), self.rot, self.qjl, out, kn, vn,
              self.lengths)
@@ -1154,6 +1244,7 @@ class PagedKVCache:
         import torch
 
         _int32_ptr(lengths, "lengths", self.batch)
+        _device_check(self.lengths, lengths=lengths)
         if at_most is not None:
             at_most = max(int(at_most), 0)
             if not self._capturing(stream):  # else nothing has run yet

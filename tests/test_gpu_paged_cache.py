@@ -459,3 +459,41 @@ def test_a_workspace_that_grows_on_another_stream():
     s.synchronize()
     ref.append(x[1][:, :, None], x[2][:, :, None])
     assert float((out - ref.attend(x[0])).abs().max()) <= TOL
+
+
+# ------------------------------------------------------------------ inputs ---
+def test_strided_inputs_are_copied():
+    """Slices of a packed projection give what contiguous inputs give."""
+    r = np.random.default_rng(11)
+    a, b = (B.PagedKVCache(2, 4, 2, n_pages=20, max_tokens=64, page=16) for _ in range(2))
+    x = _rand(r, 2, 7, 8, 128)  # [batch, tokens, q heads, k heads, v heads]
+    q, k, v = x[:, :, :4], x[:, :, 4:6].transpose(1, 2), x[:, :, 6:].transpose(1, 2)
+    assert torch.equal(a.prefill_chunk(q, k, v), b.prefill_chunk(q.contiguous(), k.contiguous(), v.contiguous()))
+    y = _rand(r, 2, 8, 256)
+    q, k, v = y[:, :4, :128], y[:, 4:6, :128], y[:, 6:, 128:]
+    assert torch.equal(a.step(q, k, v), b.step(q.contiguous(), k.contiguous(), v.contiguous()))
+    y = _rand(r, 2, 128, 8).transpose(1, 2)  # heads inside
+    assert torch.equal(a.step(y[:, :4], y[:, 4:6], y[:, 6:]),
+                       b.step(*(t.contiguous() for t in (y[:, :4], y[:, 4:6], y[:, 6:]))))
+
+
+def test_inputs_refused_before_anything_changes():
+    p = B.PagedKVCache(2, 4, 2, n_pages=20, max_tokens=64, page=16)
+    z = lambda *s, dtype=torch.float32, device="cuda": torch.zeros(s, dtype=dtype, device=device)
+    q, k, v = z(2, 4, 128), z(2, 2, 128), z(2, 2, 128)
+    bad = [(z(2, 8, 128), k, v), (z(1, 4, 128), k, v), (q, z(2, 4, 128), v), (q, k, z(2, 2, 64)), (q, k, v.bfloat16()),
+           (q.half(), k, v), (q, k.half(), v.half()), (q.cpu(), k, v), (q, k.cpu(), v.cpu()), (q, k, v, z(2, 4, 64)),
+           (q, k, v, z(2, 4, 128, dtype=torch.float16)), (q, k, v, z(2, 4, 256)[..., :128]), (q, k, v, z(2, 4, 128).cpu())]
+    for args in bad:
+        with pytest.raises(ValueError):
+            p.step(*args)
+    q, k, v = z(2, 5, 4, 128), z(2, 2, 5, 128), z(2, 2, 5, 128)
+    for args in [(z(2, 5, 8, 128), k, v), (q, z(2, 2, 4, 128), v), (q.half(), k, v), (q, k, v.bfloat16()), (q, k.cpu(), v.cpu()),
+                 (q, k, v, z(2, 5, 4, 64))]:
+        with pytest.raises(ValueError):
+            p.prefill_chunk(*args)
+    with pytest.raises(ValueError):
+        p.rollback(torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(ValueError):
+        p.fork(torch.zeros(2, dtype=torch.int32))
+    assert int(p.pool.refs.sum()) == 0 and p.lengths.tolist() == [0, 0] and p._bound == 0
