@@ -18,7 +18,7 @@
 //    O is rescaled in a tile or two of a segment, not in most of them;
 //  * the two threads of a row meet once per tile, on a hardware barrier;
 //  * P has one fp16 limb and the sign part's query one, q' keeps two: a weight
-//    is then off by at most 2^-12 of itself and a logit by about 5e-5 of
+//    is then off by at most 2^-11 of itself and a logit by about 5e-5 of
 //    ||q|| n / sqrt(d) (the sign part's rounding), far below the 2^-9 of a bf16
 //    output; all of the query operand lives in TMEM, and the place of its lo
 //    limbs in shared memory takes a second Bs buffer, so that the next tile's
@@ -37,12 +37,17 @@
 // spare time, two groups at a time, a group ahead in registers, or in halves of
 // 64 tokens was each slower: more instructions, more code in flight.)
 //
-// fp16 weights: P = 2^(l - R) nV with l in log2 units. With ev the exponent of
-// the tile's largest nV (nV < 2^ev), R is raised to max(l) + ev - 9 as soon as
-// max(l) + ev - R exceeds 15: P stays below 2^15, and a row's largest weights
-// start near 2^9, 23 binades above fp16's last normal, however small the
-// norms are. M = R and Z = sum 2^(l - R) go to the merge, which only needs them
-// to belong together.
+// fp16 weights: P = 2^(l - R) nV with l in log2 units. nV goes into the
+// exponent: the scores' factor is followed by log2 nV, P = 2^(l + log2 nV - R)
+// comes out of one exponential, and Z = sum 2^(l - R) adds P / nV. R is raised
+// to max(l + log2 nV) - 9 over the tokens that the row sees as soon as that
+// maximum exceeds R by 15: P stays below 2^15, and a row's largest weights
+// start near 2^9, 23 binades above fp16's last normal, whatever the norms are
+// and whatever the tokens that it does not see hold. M = R and Z go to the
+// merge, which only needs them to belong together. (Taking R from the largest
+// nV of the tile instead let a large norm at an unseen token push the weights
+// of small ones into fp16's subnormals.) A norm of 0 counts as 2^-64; one that
+// is not finite, or negative, makes the rows that see it NaN.
 //
 // Pages: warp 14 looks up the pages of a tile's 16-token pieces, lane k for
 // piece k, loaded one tile ahead, and fetches each run of pieces that follow one
@@ -58,6 +63,7 @@
 
 namespace tqk {
 
+constexpr float kNoNorm = 5.421010862427522e-20f;  // 2^-64, in place of a value norm of 0
 constexpr uint32_t kVwColP = 384;    // TMEM: P (64 columns); Q, S and O as in prefill_umma.cuh
 constexpr uint32_t kVwColQlo = 448;  // lo limb of q' (64 columns)
 
@@ -112,11 +118,18 @@ constexpr int vw_copies(int n, bool two) {
     return c > 32 ? 32 : c;
 }
 
+// A stage and its per-token factors: of the scores, log2 nV and 1 / nV.
+template <typename ST>
+constexpr int vw_stage_bytes() {
+    return ST::OFF_FK + 3 * kPuTok * 4;
+}
+
 constexpr int vw_log2(int n) { return n <= 1 ? 0 : 1 + vw_log2(n / 2); }
 
 template <int KB, int VB, int KB2, int VB2>
 __global__ void __launch_bounds__(kPuThreads, 1) prefill_view_kernel(const __grid_constant__ PrefillParams p) {
     using ST = PuStage<KB, VB, KB2, VB2>;
+    constexpr int SB = vw_stage_bytes<ST>();
     constexpr bool K2 = KB2 != KB, V2 = VB2 != VB;
     constexpr int KL = 1 << (2 * KB), VL = 1 << (2 * VB);
     constexpr int KL2 = K2 ? 1 << (2 * KB2) : 1, VL2 = V2 ? 1 << (2 * VB2) : 1;
@@ -138,7 +151,6 @@ __global__ void __launch_bounds__(kPuThreads, 1) prefill_view_kernel(const __gri
     __shared__ uint32_t vlut2[V2 ? VL2 * VC2 : 1];
     __shared__ float s_max[2][2][kPuRows];         // a row's two column halves, alternating by tile
     __shared__ int2 s_rows[kPuRows];               // each row's window [x, y) in the current segment
-    __shared__ __align__(16) uint32_t s_vmax[kPuStages][4];  // per stage and Bs warp: its largest |nV|, as fp16 bits
     __shared__ uint32_t s_held[kPuStages];         // bit per 16 tokens of a stage whose page holds them
     __shared__ __align__(8) uint64_t s_bar[3 * kPuStages + 10];
     __shared__ uint32_t s_tmem;
@@ -359,7 +371,7 @@ __global__ void __launch_bounds__(kPuThreads, 1) prefill_view_kernel(const __gri
             const bool first = slot >= 0 && (lane == 0 || before < 0 || slot != before + 16);
             const uint32_t held = __ballot_sync(TQ_FULL_MASK, slot >= 0), firsts = __ballot_sync(TQ_FULL_MASK, first);
             const uint32_t n = 16u * (uint32_t)__ffs((int)((firsts | ~held) >> (lane + 1)));  // tokens of the run
-            const uint32_t bar = ring_full(s), st = ring_s + (uint32_t)(s * ST::BYTES), at = 16u * (uint32_t)lane;
+            const uint32_t bar = ring_full(s), st = ring_s + (uint32_t)(s * SB), at = 16u * (uint32_t)lane;
             look_ahead();
             const int T = issued - kPuStages;
             ok = T < 0 || (!*abort_flag && vw_wait(ring_empty(s), (uint32_t)((T / kPuStages) & 1), p.err));
@@ -416,7 +428,7 @@ __global__ void __launch_bounds__(kPuThreads, 1) prefill_view_kernel(const __gri
                     *abort_flag = 1;
                     break;
                 }
-                const unsigned char* st = ring + s * ST::BYTES;
+                const unsigned char* st = ring + s * SB;
                 uint32_t w[VN + 1];
                 // the code words of this thread's token in group J
                 auto load_row = [&](int J) {
@@ -514,20 +526,20 @@ __global__ void __launch_bounds__(kPuThreads, 1) prefill_view_kernel(const __gri
                 *abort_flag = 1;
                 break;
             }
-            unsigned char* st = ring + s * ST::BYTES;
+            unsigned char* st = ring + s * SB;
             {  // the softmax's per-token factors
                 const bool valid = vw_token(s_seg[si], Tl) + tau < s_seg[si].lim && ((s_held[s] >> (tau >> 4)) & 1u);
                 const float kn = f16_bits_to_f32(reinterpret_cast<const uint16_t*>(st + ST::OFF_KN)[tau]);
-                const uint32_t vb = reinterpret_cast<const uint16_t*>(st + ST::OFF_VN)[tau] & 0x7FFFu;
-                const float vn = f16_bits_to_f32(reinterpret_cast<const uint16_t*>(st + ST::OFF_VN)[tau]);
-                // a row that does not see the token multiplies its value factor
-                // by 0, so the factor is finite here, and one that is not goes to
-                // the rows that see the token through the logit
-                const bool sound = vb < 0x7C00u;
-                reinterpret_cast<float*>(st + ST::OFF_FK)[tau] = valid ? (sound ? kn * kfac : nanf("")) : 0.0f;
-                reinterpret_cast<float*>(st + ST::OFF_FV)[tau] = valid && sound ? vn : 0.0f;
-                const uint32_t vm = __reduce_max_sync(TQ_FULL_MASK, valid && sound ? vb : 0u);
-                if (lane == 0) s_vmax[s][warp - 8] = vm;
+                const uint32_t vb = reinterpret_cast<const uint16_t*>(st + ST::OFF_VN)[tau];
+                const float vn = (vb & 0x7FFFu) != 0u ? f16_bits_to_f32((uint16_t)vb) : kNoNorm;
+                // a row that does not see the token adds 0 times its 1 / nV, so
+                // that is finite here, and a norm that is not sound goes to the
+                // rows that see the token through the logit
+                const bool sound = vb < 0x7C00u || vb == 0x8000u;
+                float* f = reinterpret_cast<float*>(st + ST::OFF_FK) + tau;
+                f[0] = valid ? (sound ? kn * kfac : nanf("")) : 0.0f;
+                f[kPuTok] = valid && sound ? __log2f(vn) : 0.0f;
+                f[2 * kPuTok] = valid && sound ? __frcp_rn(vn) : 0.0f;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(fac_full(s));
@@ -714,15 +726,14 @@ __global__ void __launch_bounds__(kPuThreads, 1) prefill_view_kernel(const __gri
                 __syncwarp();
                 if (ok && lane == 0) mbar_arrive(s_empty);  // S may take the next tile's scores
 
-                const unsigned char* st = ring + s * ST::BYTES;
+                const unsigned char* st = ring + s * SB;
                 const float4* fk = reinterpret_cast<const float4*>(st + ST::OFF_FK) + 16 * hc;
-                const float4* fv = reinterpret_cast<const float4*>(st + ST::OFF_FV) + 16 * hc;
-                // logits in log2 units: S * n_t / lam_k * scale * log2 e
+                // logits in log2 units, S * n_t / lam_k * scale * log2 e, and log2 nV
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
-                    const float4 f = fk[k];
-                    const float2 a = __fmul2_rn(make_float2(l[4 * k], l[4 * k + 1]), make_float2(f.x, f.y));
-                    const float2 b = __fmul2_rn(make_float2(l[4 * k + 2], l[4 * k + 3]), make_float2(f.z, f.w));
+                    const float4 f = fk[k], v = fk[kPuTok / 4 + k];
+                    const float2 a = __ffma2_rn(make_float2(l[4 * k], l[4 * k + 1]), make_float2(f.x, f.y), make_float2(v.x, v.y));
+                    const float2 b = __ffma2_rn(make_float2(l[4 * k + 2], l[4 * k + 3]), make_float2(f.z, f.w), make_float2(v.z, v.w));
                     l[4 * k] = a.x; l[4 * k + 1] = a.y; l[4 * k + 2] = b.x; l[4 * k + 3] = b.y;
                 }
                 {
@@ -754,36 +765,31 @@ __global__ void __launch_bounds__(kPuThreads, 1) prefill_view_kernel(const __gri
                 if (left) break;
                 // the reference (see the top): the same in both threads of the row
                 const float m = fmaxf(mloc, s_max[T & 1][hc ^ 1][r]);
-                const uint4 vm4 = *reinterpret_cast<const uint4*>(s_vmax[s]);
-                const float ev = (float)((int)(max(max(vm4.x, vm4.y), max(vm4.z, vm4.w)) >> 10) - 14);  // nV < 2^ev
                 float corr = 1.0f;
-                if (m + ev - 15.0f > R) {
-                    const float to = m + ev - 9.0f;
+                if (m - 15.0f > R) {
+                    const float to = m - 9.0f;
                     corr = ex2(R - to);  // the first reference: 0 of nothing
                     R = to;
                 }
                 const float mu = R == -INFINITY ? 0.0f : R;
+                // P as fp16, tokens 64 hc + 2j, + 1 in column 32 hc + j, and what
+                // it adds to Z; masked columns: 2^-inf = 0
                 float2 z2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                uint32_t hi[32];
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    const float2 d = __fadd2_rn(make_float2(l[2 * k], l[2 * k + 1]), make_float2(-mu, -mu));
-                    l[2 * k] = ex2(d.x);  // masked columns: 2^-inf = 0
-                    l[2 * k + 1] = ex2(d.y);
-                    z2[k & 3] = __fadd2_rn(z2[k & 3], make_float2(l[2 * k], l[2 * k + 1]));
+                for (int k = 0; k < 16; ++k) {
+                    const float4 rn = fk[kPuTok / 2 + k];
+                    const float2 d0 = __fadd2_rn(make_float2(l[4 * k], l[4 * k + 1]), make_float2(-mu, -mu));
+                    const float2 d1 = __fadd2_rn(make_float2(l[4 * k + 2], l[4 * k + 3]), make_float2(-mu, -mu));
+                    const float2 p0 = make_float2(ex2(d0.x), ex2(d0.y)), p1 = make_float2(ex2(d1.x), ex2(d1.y));
+                    z2[2 * (k & 1)] = __ffma2_rn(p0, make_float2(rn.x, rn.y), z2[2 * (k & 1)]);
+                    z2[2 * (k & 1) + 1] = __ffma2_rn(p1, make_float2(rn.z, rn.w), z2[2 * (k & 1) + 1]);
+                    const __half2 ha = __floats2half2_rn(p0.x, p0.y), hb = __floats2half2_rn(p1.x, p1.y);
+                    hi[2 * k] = *reinterpret_cast<const uint32_t*>(&ha);
+                    hi[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&hb);
                 }
                 const float2 zz = __fadd2_rn(__fadd2_rn(z2[0], z2[1]), __fadd2_rn(z2[2], z2[3]));
                 Z = fmaf(Z, corr, zz.x + zz.y);
-                // P = p * nV_t as fp16: tokens 64 hc + 2j, + 1 in column 32 hc + j
-                uint32_t hi[32];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float4 f = fv[j];
-                    const float2 a = __fmul2_rn(make_float2(l[4 * j], l[4 * j + 1]), make_float2(f.x, f.y));
-                    const float2 b = __fmul2_rn(make_float2(l[4 * j + 2], l[4 * j + 3]), make_float2(f.z, f.w));
-                    const __half2 ha = __floats2half2_rn(a.x, a.y), hb = __floats2half2_rn(b.x, b.y);
-                    hi[2 * j] = *reinterpret_cast<const uint32_t*>(&ha);
-                    hi[2 * j + 1] = *reinterpret_cast<const uint32_t*>(&hb);
-                }
                 // P(T) and the rescale of O wait for O += P(T - 1) V(T - 1) (the
                 // previous segment's last one, for a segment's first tile); a wait
                 // that runs out ends both warps at their next meeting
@@ -880,8 +886,8 @@ __global__ void __launch_bounds__(kPuThreads, 1) prefill_view_kernel(const __gri
 template <int KB, int VB, int KB2, int VB2>
 cudaError_t launch_prefill_view_t(const PrefillParams& p, cudaStream_t s) {
     auto kern = prefill_view_kernel<KB, VB, KB2, VB2>;
-    constexpr size_t smem = 2 * (size_t)kPuBsBytes + kPuVBytes + (size_t)kPuStages * PuStage<KB, VB, KB2, VB2>::BYTES;
-    static_assert(smem <= 227 * 1024 - 19 * 1024, "prefill tile buffers exceed shared memory");
+    constexpr size_t smem = 2 * (size_t)kPuBsBytes + kPuVBytes + (size_t)kPuStages * vw_stage_bytes<PuStage<KB, VB, KB2, VB2>>();
+    static_assert(smem <= 227 * 1024 - 15 * 1024, "prefill tile buffers exceed shared memory");
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     // stream-K: ceil(units x unit_tiles / tiles_per_cta) CTAs

@@ -1,0 +1,68 @@
+"""Windowed and paged attention at the edges of its number formats: norms far
+apart at tokens that a query sees and tokens that it does not."""
+
+import numpy as np
+import pytest
+import torch
+
+from online_kv_cache_quantize_gb300 import binding as B
+from online_kv_cache_quantize_gb300 import workloads as W
+from test_gpu_view import D, OUT_TOL, Pool, _built, _decode, _prefill, _seen  # noqa: F401  (_built is a fixture)
+
+pytestmark = pytest.mark.gpu
+
+MAX_F16 = 0x7BFF  # 65504
+
+
+def _scaled_values(pool, by):
+    """The pool's value norms times `by`, rounded to fp16 on both sides."""
+    n = (pool.vq["norm16"].astype(np.float64) * by).astype(np.float16)
+    pool.vq["norm16"] = n
+    pool.v.norm.copy_(torch.from_numpy(n.view(np.int16)).reshape(pool.v.norm.shape))
+
+
+@pytest.mark.parametrize("path", ["decode", "mma", "tcgen05"])
+@pytest.mark.parametrize("by", [1.0, 2.0**-18])
+@pytest.mark.parametrize("window,sinks", [(20, 0), (20, 3), (150, 8)])
+def test_large_norms_at_unseen_tokens(path, by, window, sinks):
+    """The largest finite norms at tokens that a query does not see, before its window and behind its position in
+    tiles that it reads: the output does not change in a bit, whatever the size of the norms that it sees."""
+    hkv, page, n, c = 2, 64, 384, 8
+    pool = Pool(6 * hkv, page)
+    _scaled_values(pool, by)
+    table = np.random.default_rng(1).permutation(6).astype(np.int32)[None]
+
+    def slots(tokens):
+        t = np.asarray(tokens)
+        return torch.from_numpy(np.concatenate([(table[0][t // page] * hkv + h) * page + t % page for h in range(hkv)])).cuda()
+
+    def run():
+        if path == "decode":
+            return _decode(pool, W.query_vectors((1, 8, D), dtype="bf16", seed=8), [n - 3], hkv, window, sinks, table)[0]
+        B.load().tq_prefill_force_mma_sync(1 if path == "mma" else 0)
+        try:
+            return _prefill(pool, W.query_vectors((1, c, 8, D), dtype="bf16", seed=9), [n - c], hkv, window, sinks, table)
+        finally:
+            B.load().tq_prefill_force_mma_sync(0)
+
+    clean = run()
+    if path == "decode":
+        seen = set(_seen(n - 4, n - 3, window, sinks).tolist())
+        pool.v.norm[slots([t for t in range(n) if t not in seen])] = MAX_F16
+        assert np.array_equal(run(), clean)
+        return
+    # what the oracle gives for the first and the last query (before anything is planted)
+    lim = OUT_TOL * by * float(pool.vq["norm16"].astype(np.float64).max() / by / np.sqrt(D))
+    if path == "tcgen05":
+        q = W.query_vectors((1, c, 8, D), dtype="bf16", seed=9)
+        for i in (0, c - 1):
+            t = _seen(n - c + i, n, window, sinks)
+            for h in range(8):
+                kv = h // 4
+                want = pool.oracle(q[0, i, h], (table[0][t // page] * hkv + kv) * page + t % page)
+                assert np.abs(clean[0, i, h] - want).max() <= lim, (i, h)
+    seen = set().union(*(_seen(n - c + i, n, window, sinks).tolist() for i in range(c)))
+    pool.v.norm[slots([t for t in range(n) if t not in seen])] = MAX_F16
+    assert np.array_equal(run(), clean)
+    pool.v.norm[slots([n - 1])] = MAX_F16  # the last query's own token
+    assert np.array_equal(run()[0, :-1], clean[0, :-1])
