@@ -422,6 +422,11 @@ tq_status tq_attn_prefill(const tq_prefill_args* a, void* workspace, size_t ws_b
  * gives 0; logits (decode) are written at the tokens that the query sees and
  * nowhere else. A token that a query does not see has no effect on its output,
  * whatever its page holds. Work follows the visible tokens, not the context.
+ * A prefill with out_dtype BF16 may hold its weights and the sign query in 11
+ * bits (the output has 8); with F32 it is as exact as tq_attn_prefill. Rows
+ * without window and pages may take either call: with keys of 2 or 3 bits this
+ * one measured faster (512 tokens over 8192: 161 us in bf16, 196 us in F32,
+ * tq_attn_prefill 222 us).
  * PolarQuant keys: TQ_ERR_UNSUPPORTED. A step appends token append_pos[b]
  * through the page table before it attends (an entry that holds nothing, or a
  * position past the table, skips that sequence's append); the page it writes

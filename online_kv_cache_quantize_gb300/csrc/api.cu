@@ -1596,12 +1596,12 @@ tq_status prefill_call(const tq_prefill_args* a, const tq_view* view, void* work
     cp.out_dtype = a->out_dtype == TQ_BF16 ? 1 : 0;
 
     cudaStream_t st = (cudaStream_t)stream;
-    e = view ? tqk::launch_rows_prep_view(pp, st) : tqk::launch_rows_prep(pp, st);
+    e = view ? tqk::launch_rows_prep_view(pp, a->out_dtype == TQ_F32, st) : tqk::launch_rows_prep(pp, st);
     if (e != cudaSuccess) return cuda_status(e, "tq_attn_prefill query prep");
     if (a->scan_begin && (e = cudaEventRecord((cudaEvent_t)a->scan_begin, st)) != cudaSuccess)
         return cuda_status(e, "tq_attn_prefill scan_begin");
     if (view)
-        e = pl.umma ? tqk::launch_prefill_umma_view(fp, kb, vb, two, st)
+        e = pl.umma ? tqk::launch_prefill_umma_view(fp, kb, vb, two, a->out_dtype == TQ_F32, st)
                     : tqk::launch_prefill_mma_view(fp, kb, vb, two, st);
     else
         e = pl.umma ? tqk::launch_prefill_umma(fp, kb, vb, two, st) : tqk::launch_prefill_mma(fp, kb, vb, two, st);

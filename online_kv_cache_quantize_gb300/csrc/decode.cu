@@ -251,11 +251,13 @@ __global__ void __launch_bounds__(kPrepMmaWarps * 32) rows_prep_mma_kernel(const
 // dependent of this launch: a CTA takes 16 rows at a time, four by each warp for
 // q' and four of the 16 n-tiles by each warp for u, so that few rows do not
 // leave one warp with a serial chain (256 rows: 17 us with a warp per 16 rows,
-// 4.4 us so; 16384 rows: 18 and 10.4 us). q' goes in two bf16 limbs (16 bits): u is then off by at most
-// 2^-17 of ||S_j|| ||q'||, below the fp16 rounding (2^-12) that the tcgen05 scan
-// gives it and far below the 1e-4 that logits are held to.
+// 4.4 us so; 16384 rows: 18 and 10.4 us). For a bf16 output (F32 false) u is
+// formed from two of q''s three bf16 limbs: it is then off by at most 2^-17 of
+// ||S_j|| ||q'||, below what its one fp16 limb in the tcgen05 scan drops (2^-11 of
+// itself) and far below the output's rounding.
 constexpr size_t kPrepSplitSmem = 16 * 128 * 16 + (size_t)16 * 132 * 4;
 
+template <bool F32>
 __global__ void __launch_bounds__(kPrepMmaWarps * 32) rows_prep_split_kernel(const __grid_constant__ PrepParams p) {
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     extern __shared__ __align__(16) unsigned char prep_smem[];
@@ -338,6 +340,7 @@ __global__ void __launch_bounds__(kPrepMmaWarps * 32) rows_prep_split_kernel(con
                 const uint32_t b0 = s32[((2 * ks) * 128 + n) * 4 + c], b1 = s32[((2 * ks + 1) * 128 + n) * 4 + c];
                 mma16816_bf16(acc[nt], ah, b0, b1);
                 mma16816_bf16(acc[nt], am, b0, b1);
+                if constexpr (F32) mma16816_bf16(acc[nt], al, b0, b1);
             }
         }
         const int64_t ra = r0 + g, rb = r0 + g + 8;
@@ -351,7 +354,7 @@ __global__ void __launch_bounds__(kPrepMmaWarps * 32) rows_prep_split_kernel(con
     }
 }
 
-cudaError_t launch_rows_prep_view(const PrepParams& p, cudaStream_t s) {
+cudaError_t launch_rows_prep_view(const PrepParams& p, bool f32_out, cudaStream_t s) {
     if (p.rows <= 0) return cudaSuccess;
     const bool vec_ok = (reinterpret_cast<uintptr_t>(p.q) % 16) == 0 && (reinterpret_cast<uintptr_t>(p.sgn) % 16) == 0;
     if (!(p.d == 128 && p.m == 128 && p.rht && p.s16 && p.st32 && p.qprime && p.u && !p.frag && vec_ok)) return launch_rows_prep(p, s);
@@ -361,7 +364,8 @@ cudaError_t launch_rows_prep_view(const PrepParams& p, cudaStream_t s) {
     // five CTAs fit an SM; no more than give each the same number of blocks
     const int64_t nblk = (p.rows + 15) / 16, per = (nblk + (int64_t)sms * 5 - 1) / ((int64_t)sms * 5);
     const int64_t ctas = (nblk + per - 1) / per;
-    rows_prep_split_kernel<<<(unsigned)ctas, kPrepMmaWarps * 32, kPrepSplitSmem, s>>>(p);
+    if (f32_out) rows_prep_split_kernel<true><<<(unsigned)ctas, kPrepMmaWarps * 32, kPrepSplitSmem, s>>>(p);
+    else rows_prep_split_kernel<false><<<(unsigned)ctas, kPrepMmaWarps * 32, kPrepSplitSmem, s>>>(p);
     return cudaGetLastError();
 }
 

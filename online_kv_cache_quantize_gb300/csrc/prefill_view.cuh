@@ -17,12 +17,17 @@
 //    running maximum but moves only when a weight could leave fp16's range, so
 //    O is rescaled in a tile or two of a segment, not in most of them;
 //  * the two threads of a row meet once per tile, on a hardware barrier;
-//  * P has one fp16 limb and the sign part's query one, q' keeps two: a weight
-//    is then off by at most 2^-11 of itself and a logit by about 5e-5 of
-//    ||q|| n / sqrt(d) (the sign part's rounding), far below the 2^-9 of a bf16
-//    output; all of the query operand lives in TMEM, and the place of its lo
-//    limbs in shared memory takes a second Bs buffer, so that the next tile's
-//    keys are written while this one's scores are formed;
+//  * for a bf16 output P has one fp16 limb and the sign part's query one, q'
+//    keeps two: a weight is then off by at most 2^-11 of itself and a logit by
+//    about 1e-4 of ||q|| n / sqrt(d) (the sign part's rounding); over the tokens
+//    of a window that averages to well under the 2^-9 of the output's own
+//    rounding. All of the query operand lives in TMEM then, and the place of its
+//    lo limbs in shared memory takes a second Bs buffer, so that the next tile's
+//    keys are written while this one's scores are formed. For an fp32 output (FL)
+//    P and both parts of the query have two limbs, the query's lo limbs in shared
+//    memory and one Bs buffer, as in prefill_umma.cuh: 512 tokens behind 4096 then
+//    take 126.6 us a call where the bf16 form takes 107.2 (L2 flushed), two chunks
+//    of 2048 behind 8192 1.42 ms against 1.27;
 //  * cold code is rolled and a wait is a handful of instructions;
 //  * the shared-memory pipe was 90 % busy with table lookups, operand stores and
 //    the tensor cores' reads (4.5 K of 5.0 K cycles a tile): 2-bit key codes
@@ -66,6 +71,7 @@ namespace tqk {
 constexpr float kNoNorm = 5.421010862427522e-20f;  // 2^-64, in place of a value norm of 0
 constexpr uint32_t kVwColP = 384;    // TMEM: P (64 columns); Q, S and O as in prefill_umma.cuh
 constexpr uint32_t kVwColQlo = 448;  // lo limb of q' (64 columns)
+constexpr uint32_t kVwColPlo = 448;  // FL: lo limb of P in its place
 
 // The bounded wait of the other kernels in a handful of instructions a site: the
 // clock is read at every poll, which only a wait that did not succeed at once
@@ -126,7 +132,8 @@ constexpr int vw_stage_bytes() {
 
 constexpr int vw_log2(int n) { return n <= 1 ? 0 : 1 + vw_log2(n / 2); }
 
-template <int KB, int VB, int KB2, int VB2>
+// FL: the caller's output is fp32 (see the top).
+template <int KB, int VB, int KB2, int VB2, bool FL>
 __global__ void __launch_bounds__(kPuThreads, 1) prefill_view_kernel(const __grid_constant__ PrefillParams p) {
     using ST = PuStage<KB, VB, KB2, VB2>;
     constexpr int SB = vw_stage_bytes<ST>();
@@ -136,8 +143,11 @@ __global__ void __launch_bounds__(kPuThreads, 1) prefill_view_kernel(const __gri
     constexpr int D = 128;
 
     extern __shared__ __align__(1024) unsigned char vw_smem[];
-    unsigned char* sBs = vw_smem;                  // two buffers
+    constexpr int NB = FL ? 1 : 2;                 // buffers of Bs
+    unsigned char* sBs = vw_smem;
+    unsigned char* sQlo = sBs + kPuBsBytes;        // FL: the lo limbs of the query operand
     unsigned char* sV = sBs + 2 * kPuBsBytes;
+    static_assert(kPuQloBytes == kPuBsBytes, "the lo limbs take the second buffer's place");
     unsigned char* ring = sV + kPuVBytes;
 
     __shared__ uint32_t klut[KL];
@@ -166,7 +176,7 @@ __global__ void __launch_bounds__(kPuThreads, 1) prefill_view_kernel(const __gri
     auto ring_full = [&](int s) { return bar_at(s); };
     auto ring_empty = [&](int s) { return bar_at(kPuStages + s); };
     auto fac_full = [&](int s) { return bar_at(2 * kPuStages + s); };
-    auto bs_full = [&](int b) { return bar_at(3 * kPuStages + b); };      // Bs(T) written to buffer T % 2 (4 warps)
+    auto bs_full = [&](int b) { return bar_at(3 * kPuStages + b); };      // Bs(T) written to buffer T % NB (4 warps)
     auto bs_free = [&](int b) { return bar_at(3 * kPuStages + 2 + b); };  // and read (commit)
     const uint32_t s_done = bar_at(3 * kPuStages + 4);    // S(T) complete (commit)
     const uint32_t v_full = bar_at(3 * kPuStages + 5);    // V(T) written (2 warps)
@@ -259,7 +269,8 @@ __global__ void __launch_bounds__(kPuThreads, 1) prefill_view_kernel(const __gri
     const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring);
     const uint32_t v_s = (uint32_t)__cvta_generic_to_shared(sV);
     const uint32_t bs_s = (uint32_t)__cvta_generic_to_shared(sBs);
-    auto bs_buf = [&](int T) { return bs_s + (uint32_t)(T & 1) * (uint32_t)kPuBsBytes; };
+    const uint32_t qlo_s = (uint32_t)__cvta_generic_to_shared(sQlo);
+    auto bs_buf = [&](int T) { return bs_s + (uint32_t)(T % NB) * (uint32_t)kPuBsBytes; };
 
     if (warp == 15) {
         // ======================= MMA issue (one thread) =======================
@@ -285,7 +296,8 @@ __global__ void __launch_bounds__(kPuThreads, 1) prefill_view_kernel(const __gri
                     if (T < nt) {
                         // S(T) = Q Bs(T)^T over K = 256: the key part (k-steps 0 .. 7)
                         // against both limbs of q', the sign part against kappa lam_k u
-                        ok = vw_wait(bs_full(Tg & 1), (uint32_t)((Tg >> 1) & 1), p.err) &&
+                        // (FL: both limbs, the lo ones from shared memory)
+                        ok = vw_wait(bs_full(Tg % NB), (uint32_t)((Tg / NB) & 1), p.err) &&
                              (Tg == 0 || vw_wait(s_empty, (uint32_t)((Tg - 1) & 1), p.err));
                         if (!ok) break;
                         tc_fence_after_sync();
@@ -294,11 +306,13 @@ __global__ void __launch_bounds__(kPuThreads, 1) prefill_view_kernel(const __gri
                         for (int k = 0; k < 8; ++k) {
                             const uint64_t bk = umma_desc(b0 + 256u * k, 128, 4096), bz = umma_desc(b0 + 256u * (8 + k), 128, 4096);
                             umma_f16_ta(tmem + kPuColS, tmem + kPuColQ + 8u * k, bk, idesc, k > 0);
-                            umma_f16_ta(tmem + kPuColS, tmem + kVwColQlo + 8u * k, bk, idesc, true);
+                            if constexpr (FL) umma_f16(tmem + kPuColS, umma_desc(qlo_s + 256u * k, 128, 4096), bk, idesc, true);
+                            else umma_f16_ta(tmem + kPuColS, tmem + kVwColQlo + 8u * k, bk, idesc, true);
                             umma_f16_ta(tmem + kPuColS, tmem + kPuColQ + 64u + 8u * k, bz, idesc, true);
+                            if constexpr (FL) umma_f16(tmem + kPuColS, umma_desc(qlo_s + 256u * (8 + k), 128, 4096), bz, idesc, true);
                         }
                         umma_commit(s_done);
-                        umma_commit(bs_free(Tg & 1));
+                        umma_commit(bs_free(Tg % NB));
                         last_s = Tg;
                     }
                     if (T > 0) {
@@ -308,9 +322,11 @@ __global__ void __launch_bounds__(kPuThreads, 1) prefill_view_kernel(const __gri
                         if (!ok) break;
                         tc_fence_after_sync();
 #pragma unroll 1
-                        for (int k = 0; k < 8; ++k)
-                            umma_f16_ta(tmem + kPuColO, tmem + kVwColP + 8u * k, umma_desc(v_s + 256u * k, 128, 2048), idesc,
-                                        T > 1 || k > 0);
+                        for (int k = 0; k < 8; ++k) {
+                            const uint64_t bd = umma_desc(v_s + 256u * k, 128, 2048);
+                            umma_f16_ta(tmem + kPuColO, tmem + kVwColP + 8u * k, bd, idesc, T > 1 || k > 0);
+                            if constexpr (FL) umma_f16_ta(tmem + kPuColO, tmem + kVwColPlo + 8u * k, bd, idesc, true);
+                        }
                         umma_commit(o_done);
                         last_o = Tg - 1;
                     }
@@ -321,7 +337,7 @@ __global__ void __launch_bounds__(kPuThreads, 1) prefill_view_kernel(const __gri
             // are released: the last commits cover all MMAs before them
             if (last_s >= 0) {
                 vw_wait(s_done, (uint32_t)(last_s & 1), p.err);
-                vw_wait(bs_free(last_s & 1), (uint32_t)((last_s >> 1) & 1), p.err);
+                vw_wait(bs_free(last_s % NB), (uint32_t)((last_s / NB) & 1), p.err);
             }
             if (last_o >= 0) vw_wait(o_done, (uint32_t)(last_o & 1), p.err);
         }
@@ -543,8 +559,8 @@ __global__ void __launch_bounds__(kPuThreads, 1) prefill_view_kernel(const __gri
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(fac_full(s));
-            // S(T - 2) has read this buffer
-            ok = T < 2 || vw_wait(bs_free(T & 1), (uint32_t)(((T - 2) >> 1) & 1), p.err);
+            // S(T - NB) has read this buffer
+            ok = T < NB || vw_wait(bs_free(T % NB), (uint32_t)(((T - NB) / NB) & 1), p.err);
             if (!__all_sync(TQ_FULL_MASK, ok)) {
                 *abort_flag = 1;
                 break;
@@ -629,7 +645,7 @@ __global__ void __launch_bounds__(kPuThreads, 1) prefill_view_kernel(const __gri
             fence_proxy_async_smem();  // the MMA reads Bs through the async proxy
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(bs_full(T & 1));
+                mbar_arrive(bs_full(T % NB));
                 mbar_arrive(ring_empty(s));
             }
         }
@@ -668,6 +684,7 @@ __global__ void __launch_bounds__(kPuThreads, 1) prefill_view_kernel(const __gri
             // the segment before (waited for in its tile loop) are complete ----
             if (ntiles > 0) {
                 const float su = p.qjl_scale / p.inv_lam_k;
+                const uint32_t qlo_row = qlo_s + (uint32_t)((r >> 3) * 4096 + (r & 7) * 16);  // FL
                 const float4* src = rok ? reinterpret_cast<const float4*>((hc == 0 ? p.qprime : p.u) + qrow * D) : nullptr;
 #pragma unroll 1
                 for (int h = 0; h < 4; ++h) {  // elements 32 h .. 32 h + 31
@@ -686,16 +703,19 @@ __global__ void __launch_bounds__(kPuThreads, 1) prefill_view_kernel(const __gri
                             const int e = KQ ? 8 * (k >> 2) + 4 * (k & 1) + ((k >> 1) & 1) : 2 * k;
                             split2(v[e], v[e + (KQ ? 2 : 1)], hi[k], lo[k]);
                         }
-                        tmem_st16(lane_base + kVwColQlo + 16u * h, lo);
+                        if constexpr (!FL) tmem_st16(lane_base + kVwColQlo + 16u * h, lo);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const __half2 u2 = __floats2half2_rn(v[i] * su, v[i + 16] * su);
-                            hi[i] = *reinterpret_cast<const uint32_t*>(&u2);
-                        }
+                        for (int i = 0; i < 16; ++i) split2(v[i] * su, v[i + 16] * su, hi[i], lo[i]);
+                    }
+                    if constexpr (FL) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            sts128(qlo_row + 128u * (16 * hc + 4 * h + c), lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
                     }
                     tmem_st16(lane_base + kPuColQ + 64u * hc + 16u * h, hi);
                 }
+                if constexpr (FL) fence_proxy_async_smem();  // the MMA reads the lo limbs through the async proxy
                 tmem_st_wait();
                 tc_fence_before_sync();
                 __syncwarp();
@@ -775,7 +795,7 @@ __global__ void __launch_bounds__(kPuThreads, 1) prefill_view_kernel(const __gri
                 // P as fp16, tokens 64 hc + 2j, + 1 in column 32 hc + j, and what
                 // it adds to Z; masked columns: 2^-inf = 0
                 float2 z2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                uint32_t hi[32];
+                uint32_t hi[32], lo[FL ? 32 : 1];
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
                     const float4 rn = fk[kPuTok / 2 + k];
@@ -784,9 +804,14 @@ __global__ void __launch_bounds__(kPuThreads, 1) prefill_view_kernel(const __gri
                     const float2 p0 = make_float2(ex2(d0.x), ex2(d0.y)), p1 = make_float2(ex2(d1.x), ex2(d1.y));
                     z2[2 * (k & 1)] = __ffma2_rn(p0, make_float2(rn.x, rn.y), z2[2 * (k & 1)]);
                     z2[2 * (k & 1) + 1] = __ffma2_rn(p1, make_float2(rn.z, rn.w), z2[2 * (k & 1) + 1]);
-                    const __half2 ha = __floats2half2_rn(p0.x, p0.y), hb = __floats2half2_rn(p1.x, p1.y);
-                    hi[2 * k] = *reinterpret_cast<const uint32_t*>(&ha);
-                    hi[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&hb);
+                    if constexpr (FL) {
+                        split2(p0.x, p0.y, hi[2 * k], lo[2 * k]);
+                        split2(p1.x, p1.y, hi[2 * k + 1], lo[2 * k + 1]);
+                    } else {
+                        const __half2 ha = __floats2half2_rn(p0.x, p0.y), hb = __floats2half2_rn(p1.x, p1.y);
+                        hi[2 * k] = *reinterpret_cast<const uint32_t*>(&ha);
+                        hi[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&hb);
+                    }
                 }
                 const float2 zz = __fadd2_rn(__fadd2_rn(z2[0], z2[1]), __fadd2_rn(z2[2], z2[3]));
                 Z = fmaf(Z, corr, zz.x + zz.y);
@@ -797,6 +822,7 @@ __global__ void __launch_bounds__(kPuThreads, 1) prefill_view_kernel(const __gri
                 if (!ok) continue;
                 tc_fence_after_sync();
                 tmem_st32(lane_base + kVwColP + 32u * hc, hi);
+                if constexpr (FL) tmem_st32(lane_base + kVwColPlo + 32u * hc, lo);
                 if (T > 0 && __any_sync(TQ_FULL_MASK, corr != 1.0f)) {
 #pragma unroll 1
                     for (int h = 0; h < 2; ++h) {
@@ -883,9 +909,9 @@ __global__ void __launch_bounds__(kPuThreads, 1) prefill_view_kernel(const __gri
     }
 }
 
-template <int KB, int VB, int KB2, int VB2>
+template <bool FL, int KB, int VB, int KB2, int VB2>
 cudaError_t launch_prefill_view_t(const PrefillParams& p, cudaStream_t s) {
-    auto kern = prefill_view_kernel<KB, VB, KB2, VB2>;
+    auto kern = prefill_view_kernel<KB, VB, KB2, VB2, FL>;
     constexpr size_t smem = 2 * (size_t)kPuBsBytes + kPuVBytes + (size_t)kPuStages * vw_stage_bytes<PuStage<KB, VB, KB2, VB2>>();
     static_assert(smem <= 227 * 1024 - 15 * 1024, "prefill tile buffers exceed shared memory");
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -908,6 +934,29 @@ cudaError_t launch_prefill_view_t(const PrefillParams& p, cudaStream_t s) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+// Instantiations with 1-bit keys, and with 2-bit keys or the fractional rate.
+template <bool FL>
+cudaError_t prefill_view_k1(const PrefillParams& p, int vbits, cudaStream_t s) {
+    switch (vbits) {
+        case 1: return launch_prefill_view_t<FL, 1, 1, 1, 1>(p, s);
+        case 2: return launch_prefill_view_t<FL, 1, 2, 1, 2>(p, s);
+        case 3: return launch_prefill_view_t<FL, 1, 3, 1, 3>(p, s);
+        case 4: return launch_prefill_view_t<FL, 1, 4, 1, 4>(p, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+template <bool FL>
+cudaError_t prefill_view_k2(const PrefillParams& p, int vbits, bool two, cudaStream_t s) {
+    switch (vbits) {
+        case 1: return two ? cudaErrorInvalidValue : launch_prefill_view_t<FL, 2, 1, 2, 1>(p, s);
+        case 2: return two ? launch_prefill_view_t<FL, 2, 2, 1, 1>(p, s) : launch_prefill_view_t<FL, 2, 2, 2, 2>(p, s);
+        case 3: return two ? launch_prefill_view_t<FL, 2, 3, 1, 2>(p, s) : launch_prefill_view_t<FL, 2, 3, 2, 3>(p, s);
+        case 4: return two ? launch_prefill_view_t<FL, 2, 4, 1, 3>(p, s) : launch_prefill_view_t<FL, 2, 4, 2, 4>(p, s);
+    }
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace tqk

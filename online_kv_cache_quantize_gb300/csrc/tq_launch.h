@@ -166,7 +166,7 @@ cudaError_t launch_query_prep(const PrepParams& p, cudaStream_t s);
 cudaError_t launch_rows_prep(const PrepParams& p, cudaStream_t s);
 // the same for the windowed / paged prefill: more of the work per row in
 // parallel, and the next launch on the stream may start while it runs
-cudaError_t launch_rows_prep_view(const PrepParams& p, cudaStream_t s);
+cudaError_t launch_rows_prep_view(const PrepParams& p, bool f32_out, cudaStream_t s);
 
 // One launch for the work a decode step does before its scan: the query prep
 // of pp.rows query rows (d = 128) and the quantize-on-append of k.n key and
@@ -287,7 +287,8 @@ constexpr int kPuMaxSeg = 8;  // segments (units) one CTA may touch
 constexpr int kPuMaxSegView = 48;  // windowed / paged: units can be a few tiles long
 bool prefill_umma_supported(int kbits, int vbits, bool two);
 cudaError_t launch_prefill_umma(const PrefillParams& p, int kbits, int vbits, bool two, cudaStream_t s);
-cudaError_t launch_prefill_umma_view(const PrefillParams& p, int kbits, int vbits, bool two, cudaStream_t s);
+// f32_out: the output is fp32 (the weights and the query operand in two limbs each)
+cudaError_t launch_prefill_umma_view(const PrefillParams& p, int kbits, int vbits, bool two, bool f32_out, cudaStream_t s);
 
 // The library's device error word of the current device (bits kErr* of
 // pipeline.cuh), and a kernel that waits on an mbarrier that nothing

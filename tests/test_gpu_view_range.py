@@ -66,3 +66,31 @@ def test_large_norms_at_unseen_tokens(path, by, window, sinks):
     assert np.array_equal(run(), clean)
     pool.v.norm[slots([n - 1])] = MAX_F16  # the last query's own token
     assert np.array_equal(run()[0, :-1], clean[0, :-1])
+
+
+@pytest.mark.parametrize("path", ["tcgen05", "mma"])
+@pytest.mark.parametrize("hq", [2, 8])
+def test_prefill_keeps_the_bits_of_an_fp32_output(path, hq):
+    """An fp32 output is as exact as the unwindowed call's. With 2-bit key and value codes the centroid tables are
+    exact to about 2^-22; queries, sign queries and weights in two fp16 limbs drop 2^-22 of themselves, u from three
+    bf16 limbs 2^-24. What remains is the fp32 accumulation of a logit: 32 (tcgen05, 256 products in steps of 16, two
+    limbs) to 64 additions, each dropping at most 2^-23 of a partial sum below 8 (a logit is about normal): rms
+    sqrt(64) 2^-23 8 / sqrt(3) = 4.4e-6. An output is a mean of values of rms 1 over the 8 tokens that are seen,
+    weights about 1/8: rms 4.4e-6 sqrt(8) / 8 sqrt(2) < 3e-6, and four times that is the limit. With weights in one
+    limb (2^-11 / sqrt(3) off) it would be 8e-5."""
+    hkv, page, n, c, window = 1, 64, 256, 64, 8
+    pool = Pool(4 * hkv, page, 3, 2, seed=3)
+    table = np.array([[2, 0, 3, 1]], dtype=np.int32)
+    q = W.query_vectors((1, c, hq, D), dtype="bf16", seed=31)
+    B.load().tq_prefill_force_mma_sync(1 if path == "mma" else 0)
+    try:
+        got = _prefill(pool, q, [n - c], hkv, window, 0, table)
+    finally:
+        B.load().tq_prefill_force_mma_sync(0)
+    want = np.empty_like(got, dtype=np.float64)
+    for i in range(c):
+        t = _seen(n - c + i, n, window, 0)
+        for h in range(hq):
+            want[0, i, h] = pool.oracle(q[0, i, h], table[0][t // page] * page + t % page)
+    rms = float(np.sqrt(((got - want) ** 2).mean()))
+    assert rms <= 1.2e-5, rms
