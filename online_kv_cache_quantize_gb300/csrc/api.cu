@@ -877,6 +877,7 @@ tq_status decode_prepare(const tq_decode_args* a, void* workspace, size_t ws_byt
 
     tqk::CombineParams& cp = D->cp;
     std::memset(&cp, 0, sizeof(cp));
+    cp.keep_nan = view != nullptr;
     cp.partial = part;
     cp.rows = a->batch * a->hq;
     cp.d = a->d;
@@ -1612,6 +1613,7 @@ tq_status prefill_call(const tq_prefill_args* a, const tq_view* view, void* work
     // merge, a CTA per row, in place of a warp's rounds of 8 splits
     if (view && pl.n_splits > 8 && rows <= 1024) {
         cp.err = fp.err;
+        cp.keep_nan = 1;
         return cuda_status(tqk::launch_combine(cp, st), "tq_attn_prefill merge");
     }
     return cuda_status(view ? tqk::launch_merge_view(cp, st) : tqk::launch_merge_rows(cp, st), "tq_attn_prefill merge");

@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_c
         float at = 0.0f;
         for (int q = 0; q < ug; ++q) at += s_p[q * d + tid];
         const float zt = s_zt;
-        s_a[tid] = (zt > 0.0f) ? at / zt : 0.0f;
+        s_a[tid] = (zt > 0.0f) ? at / zt : p.keep_nan ? zt : 0.0f;  // zt: 0 or NaN
     }
     __syncthreads();
     float o = 0.0f;
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kCombBulkThreads) combine_bulk_kernel(const __
     for (int k = 0; k < ns; ++k) at = fmaf(part[k * stride + tid], s_w[k], at);
     // o = s * (H a) / sqrt(d): strides 1..16 across the lanes, 32 and 64 as a
     // 4-point transform over the warps through shared memory
-    float y = z > 0.0f ? at / z : 0.0f;
+    float y = z > 0.0f ? at / z : p.keep_nan ? z : 0.0f;  // z: 0 or NaN
 #pragma unroll
     for (int h = 1; h < 32; h <<= 1) {
         const float t = __shfl_xor_sync(TQ_FULL_MASK, y, h);

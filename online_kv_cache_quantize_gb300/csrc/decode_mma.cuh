@@ -704,7 +704,9 @@ __global__ void __launch_bounds__(kMmaWarps * 32, (G > 4 ? (VW ? 3 : 2) : 4)) de
         float* out = p.partial + ((int64_t)row * p.n_splits + split) * (D + kPartPad);
         out[ci] = a;
         if (ci == 0) {
-            out[D] = mstar;
+            // VW: a row whose visible logits are all NaN has no maximum, but is
+            // not one that sees nothing (which the merge leaves out)
+            out[D] = VW && z != z && mstar == -INFINITY ? 0.0f : mstar;
             out[D + 1] = z;
         }
     }

@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(kPfWarps * 32, 2) prefill_mma_kernel(const __g
                 out[16 * (2 * c + 1) + 2 * j + h] = O[j][h][2 * row + 1] * inv_lv;
             }
         if (c == 0) {
-            out[D] = M[row];
+            out[D] = VW && z != z && M[row] == -INFINITY ? 0.0f : M[row];  // as in the decode scan
             out[D + 1] = z;
         }
     }

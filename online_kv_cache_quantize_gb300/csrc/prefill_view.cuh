@@ -880,7 +880,7 @@ __global__ void __launch_bounds__(kPuThreads, 1) prefill_view_kernel(const __gri
                 }
             }
             if (out && hc == 0) {
-                out[D] = R;
+                out[D] = zsum != zsum && R == -INFINITY ? 0.0f : R;  // all NaN is not "sees nothing", which the merge leaves out
                 out[D + 1] = zsum;
             }
             // the unit's first segment also writes the slots no CTA of the unit

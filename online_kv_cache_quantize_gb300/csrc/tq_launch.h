@@ -313,6 +313,7 @@ struct CombineParams {
     void* out;
     int out_dtype;        // 0 f32, 1 bf16
     uint32_t* err;        // device error word (null: the merge without bounded waits)
+    int keep_nan;         // launch_combine: a row whose Z is NaN is NaN (0: it is 0)
 };
 
 cudaError_t launch_combine(const CombineParams& p, cudaStream_t s);

@@ -94,3 +94,49 @@ def test_prefill_keeps_the_bits_of_an_fp32_output(path, hq):
             want[0, i, h] = pool.oracle(q[0, i, h], table[0][t // page] * page + t % page)
     rms = float(np.sqrt(((got - want) ** 2).mean()))
     assert rms <= 1.2e-5, rms
+
+
+@pytest.mark.parametrize("path", ["decode", "tcgen05", "tcgen05 f32", "mma"])
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("what", ["query", "value norm", "key norm"])
+def test_nan_reaches_the_rows_that_see_it(path, many, what):
+    """A NaN in a query, or in a norm of every token that a query sees, gives NaN in that query's output, not a
+    silent zero, and leaves the others as they were; few rows and many, which the partials are merged for
+    differently, in one split and in several."""
+    hkv, page, c, window = 1, 64, 6, 90
+    bsz = 20 if many else 1
+    n = 320
+    pool = Pool(5 * bsz * hkv, page)
+    table = np.arange(5 * bsz, dtype=np.int32).reshape(bsz, 5)
+    dtype = torch.float32 if path == "tcgen05 f32" else torch.bfloat16
+    shape = (bsz, 8, D) if path == "decode" else (bsz, c, 8, D)
+    q = W.query_vectors(shape, dtype="bf16", seed=5)
+
+    def run(q, splits):
+        if path == "decode":
+            return _decode(pool, q, [n] * bsz, hkv, window, 0, table, out_dtype=dtype, n_splits=splits)[0]
+        B.load().tq_prefill_force_mma_sync(1 if path == "mma" else 0)
+        try:
+            return _prefill(pool, q, [n - c] * bsz, hkv, window, 0, table, out_dtype=dtype, n_splits=splits)
+        finally:
+            B.load().tq_prefill_force_mma_sync(0)
+
+    for splits in (1, 2, 0):
+        clean = run(q, splits)
+        assert np.isfinite(clean).all()
+        hit = np.zeros(shape[:-1], dtype=bool)
+        if what == "query":
+            bad = q.copy()
+            at = (0, 3) if path == "decode" else (0, 2, 3)
+            bad[at][17] = np.nan
+            hit[at] = True
+            got = run(bad, splits)
+        else:
+            plane = pool.v.norm if what == "value norm" else pool.k.norm
+            keep = plane.clone()
+            plane[:5 * page] = 0x7E00  # every token of the first sequence
+            hit[0] = True
+            got = run(q, splits)
+            plane.copy_(keep)
+        assert np.isnan(got[hit]).all(), splits
+        assert np.array_equal(got[~hit], clean[~hit]), splits
