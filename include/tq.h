@@ -494,8 +494,8 @@ typedef struct {
 } tq_page_table;
 
 /* Workspace bytes of tq_pages_reserve, tq_pages_fork and tq_pages_compact on
- * this pool, for tables of at most `rows` rows (0 on error); 256-byte aligned,
- * and not shared by calls that may overlap. */
+ * this pool, for tables of at most `rows` rows (source and destination; 0 on
+ * error); 256-byte aligned, and not shared by calls that may overlap. */
 size_t tq_pages_workspace(const tq_page_pool* pool, int rows);
 
 /* Pages for the tokens lengths[b] .. lengths[b] + add[b] - 1 of every row:

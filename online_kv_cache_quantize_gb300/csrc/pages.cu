@@ -124,6 +124,17 @@ __device__ __forceinline__ void load_prefix(const PageIndex& ix, int* s_pre) {
     __syncthreads();
 }
 
+// Sum of f over the rows before `row`, in parallel over the CTA; `blocks` (may
+// be NULL) holds the sums of whole blocks of rows.
+template <typename F>
+__device__ __forceinline__ int rows_before(int row, const int32_t* blocks, F f) {
+    const int whole = blocks ? row / kRowBlock : 0;
+    int sum = 0;
+    for (int b = threadIdx.x; b < whole; b += kPageThreads) sum += blocks[b];
+    for (int r = whole * kRowBlock + (int)threadIdx.x; r < row; r += kPageThreads) sum += f(r);
+    return block_sum(sum);
+}
+
 // The r-th lowest free page (from 0), r below the number of free pages; one
 // thread, the prefix in shared memory.
 __device__ __forceinline__ int find_free(const PageIndex& ix, const int* s_pre, int r) {
@@ -291,6 +302,36 @@ __device__ __forceinline__ int64_t row_tokens(int n, const TableParams& t, int p
     return min((int64_t)max(n, 0), (int64_t)t.max_pages * page);
 }
 
+// ------------------------------------------------------------- many rows ---
+
+// blocks[b] = the sum of f over block b of the rows: one CTA each
+template <typename P>
+__global__ void __launch_bounds__(kPageThreads) row_blocks_kernel(const __grid_constant__ P p) {
+    static_assert(kRowBlock == kPageThreads, "a thread per row");
+    wait_prior_grid();
+    const int row = blockIdx.x * kRowBlock + (int)threadIdx.x;
+    const int sum = block_sum(row < p.rows() ? p.asks(row) : 0);
+    if (threadIdx.x == 0) p.blocks[blockIdx.x] = sum;
+}
+
+__global__ void __launch_bounds__(kPageThreads) fork_clear_kernel(const __grid_constant__ ForkParams p) {
+    begin_call();
+    const int r = blockIdx.x * kPageThreads + (int)threadIdx.x;
+    if (r >= p.src.rows) return;
+    p.first[r] = 0x7fffffff;
+    p.children[r] = 0;
+}
+
+__global__ void __launch_bounds__(kPageThreads) fork_parents_kernel(const __grid_constant__ ForkParams p) {
+    wait_prior_grid();
+    const int i = blockIdx.x * kPageThreads + (int)threadIdx.x;
+    if (i >= p.dst.rows) return;
+    const int r = p.parent[i];
+    if ((unsigned)r >= (unsigned)p.src.rows) return;
+    atomicMin(p.first + r, i);
+    atomicAdd(p.children + r, 1);
+}
+
 // ---------------------------------------------------------------- reserve ---
 
 // Besides empty entries, a row asks for a page where its tokens go on in the
@@ -374,9 +415,7 @@ __global__ void __launch_bounds__(kPageThreads) reserve_take_kernel(const __grid
     }
     if (want == 0) return;
     load_prefix(p.ix, s_pre);
-    int before = 0;
-    for (int r = threadIdx.x; r < row; r += kPageThreads) before += p.need[r] >> 1;
-    int rank = block_sum(before);  // this row's first request
+    int rank = rows_before(row, p.blocks, [&](int r) { return p.asks(r); });  // this row's first request
     const int free_pages = s_pre[p.ix.segs];
     const int part = (int)(len % p.pool.page);
     for (int j = j0; j < j1; j += kPageThreads) {
@@ -440,7 +479,9 @@ __global__ void __launch_bounds__(kPageThreads) fork_rows_kernel(const __grid_co
         return;
     }
     int earlier = 0;  // children of the same parent before this one
-    for (int k = threadIdx.x; k < i; k += kPageThreads) earlier |= p.parent[k] == r;
+    if (p.first) earlier = p.first[r] != i;
+    else
+        for (int k = threadIdx.x; k < i; k += kPageThreads) earlier |= p.parent[k] == r;
     const bool heir = !__syncthreads_or(earlier) && !p.keep_src;
     const int64_t n = row_tokens(p.src_lengths[r], p.src, p.pool.page);
     const int full = (int)(n / p.pool.page);
@@ -464,9 +505,14 @@ __global__ void __launch_bounds__(kPageThreads) fork_copy_kernel(const __grid_co
     wait_prior_grid();
     if ((int)blockIdx.x < p.src.rows) {
         const int r = blockIdx.x;
-        int mine = 0;
-        for (int k = threadIdx.x; k < p.dst.rows; k += kPageThreads) mine += p.parent[k] == r;
-        const int children = block_sum(mine);
+        int children;
+        if (p.children) {
+            children = p.children[r];
+        } else {
+            int mine = 0;
+            for (int k = threadIdx.x; k < p.dst.rows; k += kPageThreads) mine += p.parent[k] == r;
+            children = block_sum(mine);
+        }
         const int64_t n = row_tokens(p.src_lengths[r], p.src, p.pool.page);
         const int full = (int)(n / p.pool.page);
         // a row given up loses its own hold, which its first child takes over
@@ -484,9 +530,7 @@ __global__ void __launch_bounds__(kPageThreads) fork_copy_kernel(const __grid_co
     const int from = p.tail[i];
     if (from < 0) return;
     load_prefix(p.ix, s_pre);
-    int before = 0;
-    for (int k = threadIdx.x; k < i; k += kPageThreads) before += p.tail[k] >= 0;
-    const int rank = block_sum(before);
+    const int rank = rows_before(i, p.blocks, [&](int k) { return p.asks(k); });
     if (rank >= s_pre[p.ix.segs]) {
         if (c == 0 && threadIdx.x == 0 && p.shortage) atomicAdd(p.shortage, 1);
         return;
@@ -622,6 +666,8 @@ cudaError_t launch_after(void (*kernel)(P), unsigned ctas, size_t smem, const P&
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+unsigned ctas_of(int rows) { return (unsigned)((rows + kPageThreads - 1) / kPageThreads); }
+
 size_t prefix_smem(const PageIndex& ix) { return (size_t)(ix.segs + 1) * sizeof(int); }
 
 }  // namespace
@@ -631,14 +677,20 @@ int page_copy_chunks(int units) { return (units + kCopyUnits - 1) / kCopyUnits; 
 cudaError_t launch_pages_reserve(const ReserveParams& p, cudaStream_t s) {
     if (p.t.rows <= 0) return cudaSuccess;
     const unsigned row_ctas = (unsigned)((p.t.rows + kPageThreads / 32 - 1) / (kPageThreads / 32));
-    const cudaError_t e = launch_after(reserve_count_kernel, (unsigned)p.ix.segs + row_ctas, 0, p, s);
+    cudaError_t e = launch_after(reserve_count_kernel, (unsigned)p.ix.segs + row_ctas, 0, p, s);
     if (e != cudaSuccess) return e;
+    if (p.blocks && (e = launch_after(row_blocks_kernel<ReserveParams>, ctas_of(p.t.rows), 0, p, s)) != cudaSuccess) return e;
     return launch_after(reserve_take_kernel, (unsigned)p.t.rows, prefix_smem(p.ix), p, s);
 }
 
 cudaError_t launch_pages_fork(const ForkParams& p, cudaStream_t s) {
-    const cudaError_t e = launch_after(fork_rows_kernel, (unsigned)(p.ix.segs + p.dst.rows), 0, p, s);
-    if (e != cudaSuccess) return e;
+    cudaError_t e;
+    if (p.first && p.src.rows > 0) {
+        if ((e = launch_after(fork_clear_kernel, ctas_of(p.src.rows), 0, p, s)) != cudaSuccess) return e;
+        if ((e = launch_after(fork_parents_kernel, ctas_of(p.dst.rows), 0, p, s)) != cudaSuccess) return e;
+    }
+    if ((e = launch_after(fork_rows_kernel, (unsigned)(p.ix.segs + p.dst.rows), 0, p, s)) != cudaSuccess) return e;
+    if (p.blocks && (e = launch_after(row_blocks_kernel<ForkParams>, ctas_of(p.dst.rows), 0, p, s)) != cudaSuccess) return e;
     if (p.src.rows <= 0 && p.dst.rows <= 0) return cudaSuccess;
     return launch_after(fork_copy_kernel, (unsigned)(p.src.rows + p.dst.rows * p.chunks), prefix_smem(p.ix), p, s);
 }

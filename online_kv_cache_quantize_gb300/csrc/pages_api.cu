@@ -145,10 +145,12 @@ tq_status ints(const void* p, bool may_be_null, const std::string& what) {
     return TQ_OK;
 }
 
-// Workspace: the free-page index, one int per row, the moves and the map.
+// Workspace: the free-page index, one int per row, the moves and the map; of
+// many rows the sums of their blocks and, of a fork's parents, two ints each.
 struct PagePlan {
     int segs = 0;
-    size_t off_before = 0, off_count = 0, off_row = 0, off_move = 0, off_map = 0, off_n = 0, total = 0;
+    size_t off_before = 0, off_count = 0, off_row = 0, off_move = 0, off_map = 0, off_n = 0, off_blocks = 0, off_first = 0,
+           off_children = 0, total = 0;
 };
 
 PagePlan page_plan(int n_pages, int rows) {
@@ -161,7 +163,13 @@ PagePlan page_plan(int n_pages, int rows) {
     pl.off_move = pl.off_row + round_up((size_t)rows * 4, 256);
     pl.off_map = pl.off_move + round_up((size_t)n_pages * 8, 256);
     pl.off_n = pl.off_map + round_up((size_t)n_pages * 4, 256);
-    pl.total = pl.off_n + 256;
+    pl.off_blocks = pl.off_n + 256;
+    pl.total = pl.off_blocks;
+    if (rows > tqk::kManyRows) {
+        pl.off_first = pl.off_blocks + round_up(((size_t)rows / tqk::kRowBlock + 1) * 4, 256);
+        pl.off_children = pl.off_first + round_up((size_t)rows * 4, 256);
+        pl.total = pl.off_children + round_up((size_t)rows * 4, 256);
+    }
     return pl;
 }
 
@@ -213,6 +221,7 @@ tq_status tq_pages_reserve(const tq_pages_reserve_args* a, void* workspace, size
         p.add = a->add;
         p.add_all = a->add_all;
         p.need = (int32_t*)((char*)workspace + pl.off_row);
+        if (p.t.rows > tqk::kManyRows) p.blocks = (int32_t*)((char*)workspace + pl.off_blocks);
         p.shortage = a->shortage;
         p.granted = a->granted;
         return cuda_status(tqk::launch_pages_reserve(p, (cudaStream_t)stream), w);
@@ -257,7 +266,8 @@ tq_status tq_pages_fork(const tq_pages_fork_args* a, void* workspace, size_t ws_
         if ((s = ints(a->shortage, true, "tq_pages_fork: shortage")) != TQ_OK) return s;
         if (a->dst_lengths && ranges_meet(a->dst_lengths, (size_t)p.dst.rows * 4, a->src_lengths, (size_t)p.src.rows * 4))
             return fail(TQ_ERR_INVALID_ARG, "tq_pages_fork: src_lengths and dst_lengths overlap");
-        const PagePlan pl = page_plan(a->pool.n_pages, p.dst.rows);
+        const bool many = p.dst.rows > tqk::kManyRows;
+        const PagePlan pl = page_plan(a->pool.n_pages, many ? std::max(p.src.rows, p.dst.rows) : p.dst.rows);
         if ((s = check_ws(pl, workspace, ws_bytes, w)) != TQ_OK) return s;
         p.chunks = tqk::page_copy_chunks(p.pool.off[tqk::kPagePlanes]);
         if ((int64_t)p.src.rows + (int64_t)p.dst.rows * p.chunks + pl.segs > 0x7fffffff)
@@ -268,6 +278,11 @@ tq_status tq_pages_fork(const tq_pages_fork_args* a, void* workspace, size_t ws_
         p.dst_lengths = a->dst_lengths;
         p.keep_src = a->keep_src != 0;
         p.tail = (int32_t*)((char*)workspace + pl.off_row);
+        if (many) {
+            p.blocks = (int32_t*)((char*)workspace + pl.off_blocks);
+            p.first = (int32_t*)((char*)workspace + pl.off_first);
+            p.children = (int32_t*)((char*)workspace + pl.off_children);
+        }
         p.shortage = a->shortage;
         return cuda_status(tqk::launch_pages_fork(p, (cudaStream_t)stream), w);
     });

@@ -497,3 +497,32 @@ def test_inputs_refused_before_anything_changes():
     with pytest.raises(ValueError):
         p.fork(torch.zeros(2, dtype=torch.int32))
     assert int(p.pool.refs.sum()) == 0 and p.lengths.tolist() == [0, 0] and p._bound == 0
+
+
+# --------------------------------------------------------------- many rows ---
+@pytest.mark.parametrize("rows", [2048, 2049, 5000])
+def test_reserve_and_fork_of_many_rows(rows):
+    """Beyond a few thousand rows the requests before a row are added up by blocks: the same pages."""
+    r = np.random.default_rng(rows)
+    n_pages, mp = 3 * rows, 3
+    pool = _pool(n_pages, hkv=1)
+    m, t = Model(n_pages, 16), np.full((rows, mp), -1, dtype=np.int32)
+    lengths = r.integers(0, 30, rows)
+    table, short = _gpu(t), torch.zeros(1, dtype=torch.int32, device="cuda")
+    zero = np.zeros(rows, dtype=np.int64)
+    ws = _ws(pool, 2 * rows)
+    B.tq_pages_reserve(pool, table, _gpu(zero), _gpu(lengths), ws, shortage=short)
+    want = m.reserve(t, zero, lengths)
+    _same(pool, m, ("table", table, t), ("shortage", short, [want]))
+    m.data = _contents(pool)
+    for keep, children in ((True, rows // 3), (True, 2 * rows), (False, 2 * rows - 7)):
+        parent = r.integers(-1, rows + 1, children)
+        child, dl = pool.table(children, mp), torch.zeros(children, dtype=torch.int32, device="cuda")
+        B.tq_pages_fork(pool, table, child, _gpu(parent), _gpu(lengths), dl, ws, keep_src=keep, shortage=short)
+        got = np.full((children, mp), -1, dtype=np.int32)
+        wl, ws_short = m.fork(t, got, parent, lengths, keep)
+        _same(pool, m, ("src", table, t), ("dst", child, got), ("lengths", dl, wl), ("shortage", short, [ws_short]))
+        if keep:
+            B.tq_pages_trim(pool, child, torch.zeros_like(dl))
+            m.trim(got, np.zeros(children, dtype=np.int64), 0, 0)
+    assert np.array_equal(_contents(pool), m.data)
