@@ -570,12 +570,17 @@ def _int_check(x, what):
 
 
 def _device_check(home, **tensors):
-    """Every tensor of a call lies on the GPU that `home` lies on."""
+    """Every tensor of a call lies on the GPU that `home` lies on, and the call
+    goes to that GPU."""
+    import torch
+
     for what, t in tensors.items():
         if t is not None and t.device != home.device:
             raise ValueError(f"{what} is on {t.device}, the caches are on {home.device}")
     if home.device.type != "cuda":
         raise ValueError("the caches must be on a GPU")
+    if torch.cuda.current_device() != home.device.index:
+        raise ValueError(f"the caches are on {home.device}, the current device is cuda:{torch.cuda.current_device()}")
 
 
 def _dense_check(t, what, n, dtypes=None):

@@ -526,3 +526,19 @@ def test_reserve_and_fork_of_many_rows(rows):
             B.tq_pages_trim(pool, child, torch.zeros_like(dl))
             m.trim(got, np.zeros(children, dtype=np.int64), 0, 0)
     assert np.array_equal(_contents(pool), m.data)
+
+
+def test_calls_go_to_the_caches_device(monkeypatch):
+    """Work for one GPU is not launched while another one is current (nothing is: the check is the host's)."""
+    p = B.PagedKVCache(2, 4, 2, n_pages=20, max_tokens=64, page=16)
+    x = torch.zeros(2, 4, 128, device="cuda"), torch.zeros(2, 2, 128, device="cuda"), torch.zeros(2, 2, 128, device="cuda")
+    p.step(*x)
+    torch.cuda.synchronize()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError, match="current device is cuda:1"):
+        p.step(*x)
+    with pytest.raises(ValueError, match="current device is cuda:1"):
+        B.prepare(B.tq_pages_trim, p.pool, p.table, p.lengths)
+    monkeypatch.undo()
+    p.step(*x)
+    assert p.lengths.tolist() == [2, 2]
