@@ -13,7 +13,7 @@
 
 #include <cuda_fp16.h>
 
-#include "tq_internal.h"
+#include "entry.h"
 #include "tq_launch.h"
 
 namespace tqk {
@@ -23,7 +23,11 @@ cudaError_t launch_quantize_rht(const QuantParams& p, int dtype, int vpl, int pr
 
 namespace {
 
+using tq::aligned;
+using tq::cuda_status;
 using tq::fail;
+using tq::guarded;
+using tq::round_up;
 
 template <typename T>
 tq_status upload(T** dst, const std::vector<T>& host) {
@@ -33,8 +37,6 @@ tq_status upload(T** dst, const std::vector<T>& host) {
         return fail(TQ_ERR_CUDA, "cudaMemcpy failed while uploading a handle");
     return TQ_OK;
 }
-
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 tq_status check_rot(const tq_rotation* rot, int d) {
     if (!rot) return fail(TQ_ERR_INVALID_ARG, "rotation handle is NULL");
@@ -135,13 +137,6 @@ int vpl_for(int d) {
     if (d <= 224) return 7;
     return 8;
 }
-
-tq_status cuda_status(cudaError_t e, const char* where) {
-    if (e == cudaSuccess) return TQ_OK;
-    return fail(TQ_ERR_CUDA, std::string(where) + ": " + cudaGetErrorString(e));
-}
-
-size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 // nearest fp16 value of x (normal range), ties to even, as a double
 double fp16_round(double x) {
@@ -319,20 +314,6 @@ int64_t view_tiles(const tq_view& v, int64_t len, int64_t span, int64_t T) {
     const int64_t all = (len + T - 1) / T;
     if (v.window <= 0) return all;
     return std::min(all, ((int64_t)v.sinks + T - 1) / T + ((int64_t)v.window + span - 1 + T - 2) / T + 1);
-}
-
-// No exception (an allocation that fails) leaves a C entry.
-template <typename F>
-tq_status guarded(const char* where, F f) noexcept {
-    try {
-        return f();
-    } catch (...) {
-        try {
-            return fail(TQ_ERR_CUDA, std::string(where) + ": out of host memory");
-        } catch (...) {
-            return TQ_ERR_CUDA;
-        }
-    }
 }
 
 struct DecodePlan {

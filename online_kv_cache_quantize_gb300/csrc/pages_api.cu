@@ -5,35 +5,17 @@
 #include <cstring>
 #include <string>
 
+#include "entry.h"
 #include "pages.h"
-#include "tq_internal.h"
 #include "tq_launch.h"
 
 namespace {
 
+using tq::aligned;
+using tq::cuda_status;
 using tq::fail;
-
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
-size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-
-// No exception leaves a C entry.
-template <typename F>
-tq_status guarded(const char* where, F f) noexcept {
-    try {
-        return f();
-    } catch (...) {
-        try {
-            return fail(TQ_ERR_CUDA, std::string(where) + ": out of host memory");
-        } catch (...) {
-            return TQ_ERR_CUDA;
-        }
-    }
-}
-
-tq_status cuda_status(cudaError_t e, const std::string& where) {
-    if (e == cudaSuccess) return TQ_OK;
-    return fail(TQ_ERR_CUDA, where + ": " + cudaGetErrorString(e));
-}
+using tq::guarded;
+using tq::round_up;
 
 int sm_count() {
     int dev = 0, sms = 152;

@@ -435,83 +435,81 @@ __global__ void __launch_bounds__(kPuThreads, 1) prefill_view_kernel(const __gri
         const int J0 = 8 * vw, J1 = J0 + 8;
 #pragma unroll 1
         for (int T = 0; T < ntot; ++T) {
-            const int s = (T + kPuStages) % kPuStages;
-            if (T >= 0) {
-                bool ok = !*abort_flag && vw_wait(ring_full(s), (uint32_t)((T / kPuStages) & 1), p.err);
-                // O += P(T - 1) V(T - 1) has read V(T - 1)
-                if (ok && T > 0) ok = vw_wait(o_done, (uint32_t)((T - 1) & 1), p.err);
-                if (!__all_sync(TQ_FULL_MASK, ok)) {
-                    *abort_flag = 1;
-                    break;
-                }
-                const unsigned char* st = ring + s * SB;
-                uint32_t w[VN + 1];
-                // the code words of this thread's token in group J
-                auto load_row = [&](int J) {
-                    const unsigned char* vr = st + ST::OFF_VC + (8 * J + (lane >> 2)) * ST::VS;
-                    if constexpr (ST::VS % 16 == 0) {
+            const int s = T % kPuStages;
+            bool ok = !*abort_flag && vw_wait(ring_full(s), (uint32_t)((T / kPuStages) & 1), p.err);
+            // O += P(T - 1) V(T - 1) has read V(T - 1)
+            if (ok && T > 0) ok = vw_wait(o_done, (uint32_t)((T - 1) & 1), p.err);
+            if (!__all_sync(TQ_FULL_MASK, ok)) {
+                *abort_flag = 1;
+                break;
+            }
+            const unsigned char* st = ring + s * SB;
+            uint32_t w[VN + 1];
+            // the code words of this thread's token in group J
+            auto load_row = [&](int J) {
+                const unsigned char* vr = st + ST::OFF_VC + (8 * J + (lane >> 2)) * ST::VS;
+                if constexpr (ST::VS % 16 == 0) {
 #pragma unroll
-                        for (int i = 0; i < VN / 4; ++i) {
-                            const uint4 x = reinterpret_cast<const uint4*>(vr)[i];
-                            w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < VN / 2; ++i) {
-                            const uint2 x = reinterpret_cast<const uint2*>(vr)[i];
-                            w[2 * i] = x.x; w[2 * i + 1] = x.y;
-                        }
+                    for (int i = 0; i < VN / 4; ++i) {
+                        const uint4 x = reinterpret_cast<const uint4*>(vr)[i];
+                        w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
                     }
-                    w[VN] = 0u;
-                };
-                load_row(J0);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < VN / 2; ++i) {
+                        const uint2 x = reinterpret_cast<const uint2*>(vr)[i];
+                        w[2 * i] = x.x; w[2 * i + 1] = x.y;
+                    }
+                }
+                w[VN] = 0u;
+            };
+            load_row(J0);
 #pragma unroll 1
-                for (int J = J0; J < J1; ++J) {
-                    // Stale tokens index the tables like any other, so their values
-                    // are finite; their P is exactly 0. The loads are unconditional.
-                    uint32_t f[16];
+            for (int J = J0; J < J1; ++J) {
+                // Stale tokens index the tables like any other, so their values
+                // are finite; their P is exactly 0. The loads are unconditional.
+                uint32_t f[16];
 #pragma unroll
-                    for (int bb = 0; bb < 16; ++bb) {
-                        const bool first = !V2 || (bb & 1) == 0;
-                        const int wd = first ? VB : VB2;
-                        const int sc = 2 + vw_log2(first ? VC : VC2);  // an entry's copies are 2^sc bytes
-                        // lane q's pair is the 2 wd bits from bit base + 2 wd q on; one shift
-                        // takes them to bit sc where it can, and one three-way logical
-                        // instruction masks them and adds the lane's copy (K3 / V3, 512
-                        // tokens over 8192: 149.5 -> 143.4 us). 4-bit codes, whose lookups
-                        // meet on banks, are better spread out by two shifts (1.20 ms
-                        // against 1.25 ms at two chunks of 2048 behind 8192).
-                        const int base = code_bit<VB, VB2>(8 * bb), k = base >> 5, b = base & 31;
-                        uint32_t t;
-                        if (wd == 4) {
-                            t = b == 0 ? w[k] : __funnelshift_r(w[k], w[k + 1], b);
-                            f[bb] = lds_at<uint32_t>(first ? vtab : vtab2, ((t >> (2 * wd * q)) & 0xFFu) << sc);
-                            continue;
-                        } else if (b + 8 * wd <= 32) {  // in one word for every q
-                            t = __funnelshift_r(w[k], w[k], (uint32_t)(b - sc + 2 * wd * q));
-                        } else if (b >= sc && b - sc + 6 * wd < 32) {
-                            t = __funnelshift_r(w[k], w[k + 1], (uint32_t)(b - sc + 2 * wd * q));
-                        } else {
-                            const int c = 8;  // below 32 with 2 wd q, wd <= 3
-                            t = __funnelshift_r(w[k], w[k + 1], (uint32_t)(c + 2 * wd * q));
-                            t = b - c >= sc ? t >> (b - c - sc) : t << (sc - b + c);
-                        }
-                        const uint32_t o = (t & (((1u << (2 * wd)) - 1u) << sc)) | (first ? copy4 : copy4_2);
-                        f[bb] = lds_at<uint32_t>(first ? vlut : vlut2, o);
+                for (int bb = 0; bb < 16; ++bb) {
+                    const bool first = !V2 || (bb & 1) == 0;
+                    const int wd = first ? VB : VB2;
+                    const int sc = 2 + vw_log2(first ? VC : VC2);  // an entry's copies are 2^sc bytes
+                    // lane q's pair is the 2 wd bits from bit base + 2 wd q on; one shift
+                    // takes them to bit sc where it can, and one three-way logical
+                    // instruction masks them and adds the lane's copy (K3 / V3, 512
+                    // tokens over 8192: 149.5 -> 143.4 us). 4-bit codes, whose lookups
+                    // meet on banks, are better spread out by two shifts (1.20 ms
+                    // against 1.25 ms at two chunks of 2048 behind 8192).
+                    const int base = code_bit<VB, VB2>(8 * bb), k = base >> 5, b = base & 31;
+                    uint32_t t;
+                    if (wd == 4) {
+                        t = b == 0 ? w[k] : __funnelshift_r(w[k], w[k + 1], b);
+                        f[bb] = lds_at<uint32_t>(first ? vtab : vtab2, ((t >> (2 * wd * q)) & 0xFFu) << sc);
+                        continue;
+                    } else if (b + 8 * wd <= 32) {  // in one word for every q
+                        t = __funnelshift_r(w[k], w[k], (uint32_t)(b - sc + 2 * wd * q));
+                    } else if (b >= sc && b - sc + 6 * wd < 32) {
+                        t = __funnelshift_r(w[k], w[k + 1], (uint32_t)(b - sc + 2 * wd * q));
+                    } else {
+                        const int c = 8;  // below 32 with 2 wd q, wd <= 3
+                        t = __funnelshift_r(w[k], w[k + 1], (uint32_t)(c + 2 * wd * q));
+                        t = b - c >= sc ? t >> (b - c - sc) : t << (sc - b + c);
                     }
-                    load_row(min(J + 1, J1 - 1));  // the next group's words while this one's stores go out
-                    const uint32_t rowaddr = v_s + (uint32_t)((lane >> 3) * 2048 + J * 128 + (lane & 7) * 16);
+                    const uint32_t o = (t & (((1u << (2 * wd)) - 1u) << sc)) | (first ? copy4 : copy4_2);
+                    f[bb] = lds_at<uint32_t>(first ? vlut : vlut2, o);
+                }
+                load_row(min(J + 1, J1 - 1));  // the next group's words while this one's stores go out
+                const uint32_t rowaddr = v_s + (uint32_t)((lane >> 3) * 2048 + J * 128 + (lane & 7) * 16);
 #pragma unroll
-                    for (int bq = 0; bq < 4; ++bq)
-                        stmatrix_x4_trans(rowaddr + (uint32_t)(4 * bq * 2048), f[4 * bq], f[4 * bq + 1], f[4 * bq + 2],
-                                          f[4 * bq + 3]);
-                }
-                fence_proxy_async_smem();  // the MMA reads V through the async proxy
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(v_full);
-                    mbar_arrive(ring_empty(s));
-                }
+                for (int bq = 0; bq < 4; ++bq)
+                    stmatrix_x4_trans(rowaddr + (uint32_t)(4 * bq * 2048), f[4 * bq], f[4 * bq + 1], f[4 * bq + 2],
+                                      f[4 * bq + 3]);
+            }
+            fence_proxy_async_smem();  // the MMA reads V through the async proxy
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(v_full);
+                mbar_arrive(ring_empty(s));
             }
         }
     } else if (warp >= 8) {
