@@ -338,20 +338,30 @@ __global__ void __launch_bounds__(kPageThreads) fork_parents_kernel(const __grid
 // middle of one that another entry holds too: written there, they would
 // overwrite the other row's.
 
-// the pages [j0, j1) that the tokens length .. length + add - 1 of a row lie
-// in, and how many of them lie past the table
-__device__ __forceinline__ void reserve_range(const ReserveParams& p, int row, int* j0, int* j1, int* past, int64_t* len = nullptr,
-                                              int64_t* end = nullptr) {
-    const int64_t n = max(p.lengths[row], 0);
-    const int64_t m = n + max(p.add ? p.add[row] : p.add_all, 0);
-    if (len) {
-        *len = n;
-        *end = m;
-    }
-    const int64_t a = n / p.pool.page, b = m > n ? (m + p.pool.page - 1) / p.pool.page : a;
-    *j0 = (int)min(a, (int64_t)p.t.max_pages);
-    *j1 = (int)min(b, (int64_t)p.t.max_pages);
-    *past = (int)(b - max(a, min(b, (int64_t)p.t.max_pages)));
+// The tokens [len, end) that a row adds and the pages [j0, j1) that they lie in:
+// `part` tokens of page j0 are the row's already, `past` pages lie past the table.
+// (Both numbers stay below 2^32: 32-bit divisions.)
+struct RowRange {
+    uint32_t len, end;
+    int j0, j1, past, part;
+};
+
+__device__ __forceinline__ RowRange row_range(const ReserveParams& p, int row) {
+    const uint32_t page = (uint32_t)p.pool.page, most = (uint32_t)p.t.max_pages;
+    RowRange r;
+    r.len = (uint32_t)max(p.lengths[row], 0);
+    r.end = r.len + (uint32_t)max(p.add ? p.add[row] : p.add_all, 0);
+    const uint32_t a = r.len / page, b = r.end > r.len ? (r.end - 1u) / page + 1u : a;
+    r.j0 = (int)min(a, most);
+    r.j1 = (int)min(b, most);
+    r.past = (int)(b - max(a, min(b, most)));
+    r.part = (int)(r.len - a * page);
+    return r;
+}
+
+// the row's tokens of [len, end) that lie before page j
+__device__ __forceinline__ int tokens_before(const ReserveParams& p, const RowRange& r, int j) {
+    return (int)max((int64_t)0, min((int64_t)r.end, (int64_t)j * p.pool.page) - r.len);
 }
 
 // CTAs [0, segs): the index; the others: one row each, its requests counted
@@ -365,14 +375,13 @@ __global__ void __launch_bounds__(kPageThreads) reserve_count_kernel(const __gri
     // one warp per row
     const int row = (blockIdx.x - p.ix.segs) * (kPageThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (row >= p.t.rows) return;
-    int j0, j1, past, n = 0;
-    reserve_range(p, row, &j0, &j1, &past);
-    const bool part = max(p.lengths[row], 0) % p.pool.page != 0;
+    const RowRange rr = row_range(p, row);
+    int n = 0;
     bool own = false;  // lane 0: the half-filled last page is another entry's too, the row wants one of its own
-    for (int j = j0 + lane; j < j1; j += 32) {
+    for (int j = rr.j0 + lane; j < rr.j1; j += 32) {
         const int e = p.t.e[row * p.t.stride + j];
         bool ask = !page_ok(e, p.pool.n_pages);
-        if (j == j0 && part && !ask) ask = own = p.pool.refs[e] > 1;
+        if (j == rr.j0 && rr.part && !ask) ask = own = p.pool.refs[e] > 1;
         n += ask ? 1 : 0;
     }
     n = __reduce_add_sync(TQ_FULL_MASK, n);
@@ -402,28 +411,25 @@ __global__ void __launch_bounds__(kPageThreads) reserve_take_kernel(const __grid
     __shared__ int s_from, s_to, s_gap;
     wait_prior_grid();
     const int row = blockIdx.x;
-    int j0, j1, past;
-    int64_t len, end;
-    reserve_range(p, row, &j0, &j1, &past, &len, &end);
-    const int want = p.need[row] >> 1;
-    const bool own = p.need[row] & 1;
+    const int need = p.need[row], want = need >> 1;
+    const bool own = need & 1;
+    const RowRange rr = row_range(p, row);
     if (threadIdx.x == 0) {
-        if (past > 0 && p.shortage) atomicAdd(p.shortage, past);
+        if (rr.past > 0 && p.shortage) atomicAdd(p.shortage, rr.past);
         s_from = s_to = -1;
-        s_gap = j1;  // the first page the row does not hold after the call
-        if (want == 0 && p.granted) p.granted[row] = (int)max((int64_t)0, min(end, (int64_t)j1 * p.pool.page) - len);
+        s_gap = rr.j1;  // the first page the row does not hold after the call
+        if (want == 0 && p.granted) p.granted[row] = tokens_before(p, rr, rr.j1);
     }
     if (want == 0) return;
     load_prefix(p.ix, s_pre);
     int rank = rows_before(row, p.blocks, [&](int r) { return p.asks(r); });  // this row's first request
     const int free_pages = s_pre[p.ix.segs];
-    const int part = (int)(len % p.pool.page);
-    for (int j = j0; j < j1; j += kPageThreads) {
+    for (int j = rr.j0; j < rr.j1; j += kPageThreads) {
         const int jj = j + (int)threadIdx.x;
         int32_t* e = p.t.e + row * p.t.stride + jj;
-        const int old = jj < j1 ? *e : -1;
-        const bool copy = own && jj == j0;
-        const bool ask = jj < j1 && (copy || !page_ok(old, p.pool.n_pages));
+        const int old = jj < rr.j1 ? *e : -1;
+        const bool copy = own && jj == rr.j0;
+        const bool ask = jj < rr.j1 && (copy || !page_ok(old, p.pool.n_pages));
         int total;
         const int r = rank + block_prefix(ask ? 1 : 0, &total);
         if (ask) {
@@ -436,7 +442,7 @@ __global__ void __launch_bounds__(kPageThreads) reserve_take_kernel(const __grid
                 if (p.shortage) atomicAdd(p.shortage, 1);
             }
             *e = got;
-            if (jj == j0 && part) {
+            if (jj == rr.j0 && rr.part) {
                 if (copy) s_from = old;
                 s_to = got;
             }
@@ -444,10 +450,10 @@ __global__ void __launch_bounds__(kPageThreads) reserve_take_kernel(const __grid
         rank += total;
     }
     __syncthreads();
-    if (threadIdx.x == 0 && p.granted) p.granted[row] = (int)max((int64_t)0, min(end, (int64_t)s_gap * p.pool.page) - len);
+    if (threadIdx.x == 0 && p.granted) p.granted[row] = tokens_before(p, rr, s_gap);
     const int from = s_from, to = s_to;
     if (to >= 0) {
-        if (from < 0) clear_tokens(p.pool, to, part);
+        if (from < 0) clear_tokens(p.pool, to, rr.part);
         else
             for (int c = 0; c * kCopyUnits < p.pool.off[kPagePlanes]; ++c) copy_chunk(p.pool, p.pool, from, to, c);
     }
