@@ -25,22 +25,23 @@
 //    lo limbs in shared memory takes a second Bs buffer, so that the next tile's
 //    keys are written while this one's scores are formed. For an fp32 output (FL)
 //    P and both parts of the query have two limbs, the query's lo limbs in shared
-//    memory and one Bs buffer, as in prefill_umma.cuh: 512 tokens behind 4096 then
-//    take 126.6 us a call where the bf16 form takes 107.2 (L2 flushed), two chunks
-//    of 2048 behind 8192 1.42 ms against 1.27;
+//    memory and one Bs buffer, as in prefill_umma.cuh: the scan of 512 tokens
+//    behind 4096 then takes 110 us where the bf16 form takes 90, the call 127
+//    against 107 us (L2 flushed), two chunks of 2048 behind 8192 1.42 against 1.27 ms;
 //  * cold code is rolled and a wait is a handful of instructions;
 //  * the shared-memory pipe was 90 % busy with table lookups, operand stores and
 //    the tensor cores' reads (4.5 K of 5.0 K cycles a tile): 2-bit key codes
 //    become fp16 pairs by byte permutes instead of lookups, and the value tables
 //    hold a copy of each entry per bank.
-// Measured (GB300, K3 / V3, 32 query / 8 KV heads): a 512-token chunk over 32768
-// tokens in full 478 us for the scan (prefill_umma.cuh 615), behind a window of
-// 4096 tokens 90 us (the call 100.5 us); two 2048-token chunks behind 8192 tokens with 4-bit values
-// 1.19 ms, with 3-bit ones 1.03 ms. What bounds it now: the chain of a tile's
-// values, about 3 K cycles for two warps to write V after O has read the one before
-// (the instructions of its lookups), then 1.0 K for O. (V in four more warps'
-// spare time, two groups at a time, a group ahead in registers, or in halves of
-// 64 tokens was each slower: more instructions, more code in flight.)
+// Measured (GB300, K3 / V3, 32 query / 8 KV heads, bf16 output): a 512-token chunk
+// over 32768 tokens in full 491 us for the scan (prefill_umma.cuh 615), over 8192
+// 145 us, behind a window of 4096 tokens 90 us (the call 99.7 us); two 2048-token
+// chunks behind 8192 tokens with 4-bit values 1.24 ms, with 3-bit ones 1.06 ms.
+// What bounds it now: the chain of a tile's values, about 3 K cycles for two warps
+// to write V after O has read the one before (the instructions of its lookups),
+// then 1.0 K for O. (V in four more warps' spare time, two groups at a time, a
+// group ahead in registers, or in halves of 64 tokens was each slower: more
+// instructions, more code in flight.)
 //
 // fp16 weights: P = 2^(l - R) nV with l in log2 units. nV goes into the
 // exponent: the scores' factor is followed by log2 nV, P = 2^(l + log2 nV - R)
@@ -51,14 +52,16 @@
 // and whatever the tokens that it does not see hold. M = R and Z go to the
 // merge, which only needs them to belong together. (Taking R from the largest
 // nV of the tile instead let a large norm at an unseen token push the weights
-// of small ones into fp16's subnormals.) A norm of 0 counts as 2^-64; one that
+// of small ones into fp16's subnormals. The third factor that the softmax reads
+// per token, 1 / nV, costs 2.6 % where 4-bit values keep shared memory busiest:
+// two 2048-token chunks 1.23 -> 1.26 ms a call.) A norm of 0 counts as 2^-64; one that
 // is not finite, or negative, makes the rows that see it NaN.
 //
 // Pages: warp 14 looks up the pages of a tile's 16-token pieces, lane k for
 // piece k, loaded one tile ahead, and fetches each run of pieces that follow one
 // another with one copy per plane. It does nothing else: this takes it 2.2 K
 // cycles a tile, and took 1.2 K of the thread that feeds the tensor cores (which
-// has no time for it), while two warps write V in 2.5 K.
+// has no time for it), while two warps write V in about 3 K.
 //
 // Warp roles: 0-7 softmax (two threads per row), 8-11 Bs (thread = token), 12
 // and 13 V, 14 copies, 15 MMA issue (one thread).
