@@ -509,7 +509,9 @@ size_t tq_pages_workspace(const tq_page_pool* pool, int rows);
  * given back) has those cleared to zero vectors, which queries see; a row that
  * is to go on without them is cut back to the page's start first. granted tells
  * how many of the row's add tokens have a page: those up to the first that has
- * none. A row whose length grows by that, and not by add, loses nothing else. */
+ * none. Where no page is free for the row's own last tokens it is their number
+ * below 0. A row whose length changes by that, and not by add, holds all of its
+ * tokens. */
 typedef struct {
     tq_page_pool pool;
     tq_page_table table;

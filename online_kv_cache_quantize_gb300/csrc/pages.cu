@@ -359,9 +359,13 @@ __device__ __forceinline__ RowRange row_range(const ReserveParams& p, int row) {
     return r;
 }
 
-// the row's tokens of [len, end) that lie before page j
-__device__ __forceinline__ int tokens_before(const ReserveParams& p, const RowRange& r, int j) {
-    return (int)max((int64_t)0, min((int64_t)r.end, (int64_t)j * p.pool.page) - r.len);
+// granted: the row's tokens of [len, end) before page j1, the last, or `gap`, the
+// first page that the row does not hold after the call (j1: there is none). In
+// the page of its own last tokens that is as many below 0.
+__device__ __forceinline__ int row_granted(const ReserveParams& p, const RowRange& r, int gap) {
+    const int64_t page = p.pool.page;
+    if (gap < r.j1) return (int)(gap * page - r.len);
+    return (int)max((int64_t)0, min((int64_t)r.end, r.j1 * page) - r.len);
 }
 
 // CTAs [0, segs): the index; the others: one row each, its requests counted
@@ -418,7 +422,7 @@ __global__ void __launch_bounds__(kPageThreads) reserve_take_kernel(const __grid
         if (rr.past > 0 && p.shortage) atomicAdd(p.shortage, rr.past);
         s_from = s_to = -1;
         s_gap = rr.j1;  // the first page the row does not hold after the call
-        if (want == 0 && p.granted) p.granted[row] = tokens_before(p, rr, rr.j1);
+        if (want == 0 && p.granted) p.granted[row] = row_granted(p, rr, rr.j1);
     }
     if (want == 0) return;
     load_prefix(p.ix, s_pre);
@@ -450,7 +454,7 @@ __global__ void __launch_bounds__(kPageThreads) reserve_take_kernel(const __grid
         rank += total;
     }
     __syncthreads();
-    if (threadIdx.x == 0 && p.granted) p.granted[row] = tokens_before(p, rr, s_gap);
+    if (threadIdx.x == 0 && p.granted) p.granted[row] = row_granted(p, rr, s_gap);
     const int from = s_from, to = s_to;
     if (to >= 0) {
         if (from < 0) clear_tokens(p.pool, to, rr.part);

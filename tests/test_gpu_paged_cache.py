@@ -238,6 +238,34 @@ def test_fork_without_a_free_page():
     _counts_match(p)
 
 
+def test_a_copy_without_a_free_page():
+    """Rows back below their fork that find no page for a copy of their last one lose its tokens, and are cut."""
+    r = np.random.default_rng(12)
+    p = B.PagedKVCache(3, 4, 2, n_pages=8, max_tokens=96, page=16)
+    ref = Histories(p, 96)
+    k, v = _rand(r, 3, 2, 32, 128), _rand(r, 3, 2, 32, 128)
+    p.prefill_chunk(_rand(r, 3, 32, 4, 128), k, v)
+    ref.append(k, v)
+    p.fork(_gpu([0, 0, 2]))
+    ref.fork([0, 0, 2])
+    p.rollback(_gpu([26, 20, 32]))  # both in the shared second page
+    ref.n = [26, 20, 32]
+    others = p.pool.refs == 0
+    p.pool.refs[others] = 1  # somebody else's
+    ref.n = [16, 16, 32]
+    _lossy_step(p, ref, r, 4, [0, 0, 0])
+    assert int(p.shortage) == 3
+    p.pool.refs[others] = 0
+    for _ in range(16):
+        _lossy_step(p, ref, r, 4, [1, 1, 1])
+    assert int(p.shortage) == 3
+    # 32, 32 and 48 tokens: a shared page, two of their own and three are in use, two are left for three rows
+    for _ in range(4):
+        _lossy_step(p, ref, r, 4, [1, 1, 0])
+    assert int(p.shortage) == 7
+    _counts_match(p)
+
+
 def test_a_page_taken_for_lost_tokens_is_cleared():
     """An entry filled in the middle of its page: the tokens before are zero vectors, not what the page held."""
     for mode in ("prod", "polar"):
@@ -273,6 +301,12 @@ def test_granted_tokens():
     # free: 3, 4. Row 0 takes both (tokens 10 .. 47 of 10 .. 49); rows 1 and 2 find none
     assert table.tolist() == [[0, 3, 4], [-1, -1, 1], [2, -1, -1], [-1, -1, -1]]
     assert granted.tolist() == [38, 0, 0, 0]
+    # no page for the rows' own last tokens: an empty entry, and a shared page that finds no copy
+    table = _gpu([[0, -1], [-1, -1], [1, -1], [1, -1]])
+    pool.refs.copy_(_gpu([1, 2, 1, 1, 1]))
+    B.tq_pages_reserve(pool, table, _gpu([15, 5, 9, 16]), _gpu([3, 20, 1, 2]), _ws(pool, 4), granted=granted)
+    assert granted.tolist() == [1, -5, -9, 0] and table.tolist() == [[0, -1], [-1, -1], [-1, -1], [1, -1]]
+    assert pool.refs.tolist() == [1, 1, 1, 1, 1]
 
 
 # -------------------------------------------------- captured calls and others ---
@@ -542,3 +576,37 @@ def test_calls_go_to_the_caches_device(monkeypatch):
     monkeypatch.undo()
     p.step(*x)
     assert p.lengths.tolist() == [2, 2]
+
+
+def test_captured_chunks_rollbacks_and_compactions():
+    """Everything but a fork in graphs, replayed with other inputs and lengths."""
+    r = np.random.default_rng(13)
+    p = B.PagedKVCache(2, 4, 2, n_pages=24, max_tokens=96, page=16, window=40, sinks=3, max_rollback=8)
+    ref = Histories(p, 96 + 64)
+    bufs = [_rand(r, 2, 6, 4, 128), _rand(r, 2, 2, 6, 128), _rand(r, 2, 2, 6, 128)]
+    to = _gpu([0, 0])
+
+    def run():
+        out = p.prefill_chunk(*bufs)
+        p.rollback(to)
+        p.compact()
+        return out
+
+    run()  # outside first, and back to nothing
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = run()
+    for i in range(12):
+        for b in bufs:
+            b.copy_(_rand(r, *b.shape))
+        n = ref.n
+        to.copy_(_gpu([n[0] + 6 - i % 3, n[1] + 6 - (i + 1) % 4]))
+        g.replay()
+        ref.append(bufs[1], bufs[2])
+        # the last query of each row sees all of its window
+        err = float((out[:, -1] - ref.attend(bufs[0][:, -1].contiguous())).abs().max())
+        assert err <= TOL, (i, err)
+        ref.n = to.tolist()
+        assert p.lengths.tolist() == ref.n
+    assert int(p.shortage) == 0
+    _counts_match(p)
