@@ -590,7 +590,7 @@ def _dense_check(t, what, n, dtypes=None):
     names = dtypes or (torch.float32, torch.bfloat16)
     if t.dtype not in names:
         raise ValueError(f"{what} must be of {' or '.join(str(x) for x in names)}")
-    if not t.is_contiguous() or t.numel() != n:
+    if not t.is_contiguous() or t.numel() < n:
         raise ValueError(f"{what} must be contiguous and hold {n} values")
 
 
@@ -800,7 +800,8 @@ def tq_pages_reserve(pool, table, lengths, add, workspace, shortage=None, grante
     """Pages for the `add` tokens (an int, or device int32 per row) behind each
     row's lengths[b] tokens; a half-filled last page that other rows hold too is
     replaced by a copy. granted (device int32 per row): how many of these tokens
-    lie in pages the row holds, from the first on."""
+    lie in pages the row holds, from the first on; below 0 the tokens that the
+    row lost with its last page."""
     a = tq_pages_reserve_args(pool.struct(), _table_struct(table), _int32_ptr(lengths, "lengths", table.shape[0]))
     if isinstance(add, int):
         a.add_all = _int_check(add, "add")
@@ -1194,14 +1195,15 @@ class PagedKVCache:
 
         if tuple(q.shape) != (self.batch, self.hq, self.d):
             raise ValueError("q must be [batch, hq, d]")
-        if not tuple(k_new.shape) == tuple(v_new.shape) == (self.batch, self.hkv, self.d):
+        n = self.batch * self.hkv * self.d
+        if k_new.shape[-1:] != v_new.shape[-1:] or k_new.numel() != n or v_new.numel() != n:
             raise ValueError("k_new and v_new must be [batch, hkv, d]")
         self._inputs_check(q, k_new, v_new, out)
         self._reserve(1, stream)
         with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
             if out is None:
                 out = torch.empty((self.batch, self.hq, self.d), dtype=torch.float32, device=q.device)
-            q, kn, vn = q.contiguous(), k_new.contiguous(), v_new.contiguous()
+            q, kn, vn = q.contiguous(), k_new.contiguous(), v_new.contiguous()  # the calls know no strides
             new_lens = self.lengths + self._granted
         a = (q, self.k, self.v, new_lens, self._longest(1), self.rot, self.qjl, out, kn, vn,
              self.lengths)

@@ -140,3 +140,41 @@ def test_nan_reaches_the_rows_that_see_it(path, many, what):
             plane.copy_(keep)
         assert np.isnan(got[hit]).all(), splits
         assert np.array_equal(got[~hit], clean[~hit]), splits
+
+
+@pytest.mark.parametrize("path", ["decode", "tcgen05", "tcgen05 f32", "mma"])
+def test_value_norms_of_zero(path):
+    """Tokens of zero values take their weight and add nothing, be it all of a sequence's tokens or the ones that
+    most of the weight goes to; a row that sees nothing else is 0 to far below any other output (2^-60)."""
+    hkv, page, c, n = 1, 64, 6, 128
+    pool = Pool(4 * hkv, page)
+    table = np.arange(4, dtype=np.int32).reshape(2, 2)
+    dtype = torch.float32 if path == "tcgen05 f32" else torch.bfloat16
+    shape = (2, 8, D) if path == "decode" else (2, c, 8, D)
+    q = W.query_vectors(shape, dtype="bf16", seed=5)
+    nv = pool.vq["norm16"].copy()
+    nv[:2 * page] = 0  # the first sequence
+    r = np.random.default_rng(2)
+    some = 2 * page + r.permutation(2 * page)[:100]
+    nv[some] = 0  # most of the second one
+    pool.vq["norm16"] = nv
+    pool.v.norm.copy_(torch.from_numpy(nv.astype(np.float16).view(np.int16)).reshape(pool.v.norm.shape))
+    if path == "decode":
+        got = _decode(pool, q, [n, n], hkv, 0, 0, table, out_dtype=dtype)[0]
+        pos = [n - 1]
+        got = got[:, None]
+    else:
+        B.load().tq_prefill_force_mma_sync(1 if path == "mma" else 0)
+        try:
+            got = _prefill(pool, q, [n - c] * 2, hkv, 0, 0, table, out_dtype=dtype)
+        finally:
+            B.load().tq_prefill_force_mma_sync(0)
+        pos = list(range(n - c, n))
+    assert np.abs(got[0]).max() <= 2.0**-60
+    qq = q[:, None] if path == "decode" else q
+    for i, at in enumerate(pos):
+        t = np.arange(at + 1)
+        for h in range(8):
+            want = pool.oracle(qq[1, i, h], 2 * page + t)
+            lim = OUT_TOL + (2.0**-8 * np.abs(want) if dtype == torch.bfloat16 else 0)
+            assert (np.abs(got[1, i, h] - want) <= lim).all(), (i, h)
