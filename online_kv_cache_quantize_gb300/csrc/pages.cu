@@ -398,7 +398,7 @@ __device__ __forceinline__ void clear_tokens(const PoolParams& pool, int64_t pg,
     const int slots = pool.slots;
 #pragma unroll
     for (int q = 0; q < kPagePlanes; ++q) {
-        if (pool.units[q] * 16 != 2 * slots) continue;
+        if (pool.units[q] != slots / 8) continue;
         uint16_t* x = reinterpret_cast<uint16_t*>(pool.base[q]) + pg * slots;
         for (int i = threadIdx.x; i < slots; i += kPageThreads)
             if (i % pool.page < tokens) x[i] = 0;

@@ -7,7 +7,8 @@ import torch
 
 from online_kv_cache_quantize_gb300 import binding as B
 from online_kv_cache_quantize_gb300 import workloads as W
-from test_gpu_view import D, OUT_TOL, Pool, _built, _decode, _prefill, _seen  # noqa: F401  (_built is a fixture)
+from test_gpu_view import (D, OUT_TOL, Pool, _built, _check_prefill, _decode, _paged_table, _prefill,  # noqa: F401
+                           _seen)
 
 pytestmark = pytest.mark.gpu
 
@@ -178,3 +179,52 @@ def test_value_norms_of_zero(path):
             want = pool.oracle(qq[1, i, h], 2 * page + t)
             lim = OUT_TOL + (2.0**-8 * np.abs(want) if dtype == torch.bfloat16 else 0)
             assert (np.abs(got[1, i, h] - want) <= lim).all(), (i, h)
+
+
+# --------------------------------------------- the prefill of a bf16 output ---
+@pytest.mark.parametrize("kbits,vbits,bits2", [(2, 1, None), (2, 2, None), (2, 3, None), (2, 4, None), (3, 1, None), (3, 2, None),
+                                               (3, 3, None), (3, 4, None), (3, 2, (2, 1)), (3, 3, (2, 2)), (3, 4, (2, 3))])
+@pytest.mark.parametrize("kind", ["rht", "dense"])
+def test_bf16_prefill_widths(kbits, vbits, bits2, kind):
+    """Every width of the tcgen05 scan with the output type that holds its weights in one limb, over several tiles,
+    missing pages among them."""
+    r = np.random.default_rng(kbits * 10 + vbits)
+    hkv, page, start, c = 2, 80, 300, 70
+    need = -(-(start + c) // page) + 1
+    pool = Pool(need * hkv, page, kbits, vbits, kind, bits2=bits2)
+    table = _paged_table(r, [start + c], page, need)
+    table[0, 1] = -1
+    q = W.query_vectors((1, c, 2 * hkv, D), dtype="bf16", seed=14)
+    got = _prefill(pool, q, [start], hkv, 200, 9, table, torch.bfloat16, torch.bfloat16)
+    _check_prefill(pool, q, [start], hkv, 200, 9, table, got, bf16=True, every=23)
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (16, 4), (130, 17), (300, 200), (10**9, 10**9)])
+@pytest.mark.parametrize("page", [None, 16, 48, 128])
+def test_bf16_prefill_masks(window, sinks, page):
+    r = np.random.default_rng(window % 1000 + sinks % 1000 + (page or 0))
+    hkv, starts, c = 2, [600, 0, 131], 21
+    lens = [s + c for s in starts]
+    if page is None:
+        pool, table = Pool(len(lens) * hkv, 640), None
+    else:
+        need = sum(-(-n // page) for n in lens) + 2
+        pool = Pool(need * hkv, page)
+        table = _paged_table(r, lens, page, need)
+    q = W.query_vectors((3, c, 4 * hkv, D), dtype="bf16", seed=12)
+    got = _prefill(pool, q, starts, hkv, window, sinks, table, torch.bfloat16, torch.bfloat16)
+    _check_prefill(pool, q, starts, hkv, window, sinks, table, got, bf16=True, every=4)
+
+
+@pytest.mark.parametrize("n_splits", [0, 1, 3, 8, 9])
+def test_bf16_prefill_splits(n_splits):
+    """Units in several splits, CTAs that go through several units."""
+    r = np.random.default_rng(n_splits)
+    hkv, page, c, group = 2, 64, 270, 4
+    start = 128 * 9 - 20
+    need = -(-(start + c) // page)
+    pool = Pool(need * hkv, page)
+    table = _paged_table(r, [start + c], page, need, holes=0.1)
+    q = W.query_vectors((1, c, group * hkv, D), dtype="bf16", seed=13)
+    got = _prefill(pool, q, [start], hkv, 0, 0, table, torch.bfloat16, torch.bfloat16, n_splits)
+    _check_prefill(pool, q, [start], hkv, 0, 0, table, got, bf16=True, every=45)
